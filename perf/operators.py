@@ -281,6 +281,7 @@ def _append_plain(s, x, codes, scales):
     was = torch.where((older > 0)[:, None], scales, torch.zeros_like(scales))
     # (a tensor of 127s: torch multiplies by the rounded inverse of a plain number)
     now = torch.where(touched[:, None], torch.maximum(was, peak / torch.full_like(peak, 127)), scales)
+    now = torch.where(touched[:, None] & (now < 2.0 ** -60), torch.zeros_like(now), now)
     inv = torch.where(now > 0, 1 / now, torch.zeros_like(now))
     grown = (now > scales) & (older > 0)[:, None] & touched[:, None]
     kept = torch.where(grown, was * inv, torch.ones_like(now))
@@ -398,6 +399,8 @@ def _append_exact(case, x, codes, scales, table, lens, new):
                 if lo:
                     before = scales[page, h]
                     d = max(d, before)
+                if d < 2.0 ** -60:
+                    d = f(0)
                 inv = f(1) / d if d > 0 else f(0)
                 if lo and d > before:
                     codes[page, h] = nearest(codes[page, h].astype(f) * (before * inv))
