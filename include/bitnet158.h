@@ -69,7 +69,7 @@ typedef enum bitnet_status {
     BITNET_ERR_MISALIGNED = 3,        /* a pointer breaks the alignment rule above       */
     BITNET_ERR_CUDA = 4,              /* a CUDA runtime call or launch failed            */
     BITNET_ERR_TIMEOUT = 5,           /* a device-side bounded wait gave up              */
-    BITNET_ERR_RANGE = 6,             /* reserved: input outside the numeric contract    */
+    BITNET_ERR_RANGE = 6,             /* device arrays describe something that is not there */
     BITNET_ERR_WORKSPACE = 7          /* workspace missing or smaller than required      */
 } bitnet_status;
 
@@ -423,6 +423,140 @@ bitnet_status bitnet_decode_chain(const bitnet_chain_step *steps, int n_steps, c
                                   bitnet_stream_t stream);
 
 /* ----------------------------------------------------------------------
+ * Key/value cache in 8 bits, in pages: a page holds page_tokens tokens of
+ * one sequence, for every key/value head head_dim int8 codes per token and
+ * ONE fp32 scale for keys and one for values; value = code * scale.
+ * (The pages on BitNet b1.58 give no attention formula; the cache keeps the
+ * 8 bits of the activations.)
+ *
+ *   k_codes, v_codes   [num_pages][heads][page_tokens][head_dim], 16-byte
+ *                      aligned; k_scales, v_scales [num_pages][heads].
+ *   page_tokens        16, 32, 64 or 128; head_dim 64 or 128; heads 1..32767.
+ * A scale is 0 (all codes of the page and head are 0) or at least 2^-60.
+ * The struct is read during the call only.
+ *
+ * A batch of B sequences is given by device arrays:
+ *   pages    [B][max_pages] int32: position p of sequence b lies in row
+ *            p % page_tokens of page pages[b][p / page_tokens].  Entries
+ *            behind a sequence's last position are not read.  Sequences may
+ *            share pages that only attention reads; a page that
+ *            bitnet_kv_append writes belongs to one sequence.
+ *   lens     [B] int32: tokens of the sequence, the new ones among them.
+ *   offsets  [B + 1] int32: rows offsets[b] .. offsets[b + 1] - 1 of the new
+ *            tokens' arrays are sequence b's last ones, in order, the last
+ *            row at position lens[b] - 1.  NULL: one row per sequence (T ==
+ *            B).  Rows behind offsets[B] belong to no sequence.
+ *   max_new  the most new rows of a sequence, as the launch is sized by it;
+ *            results do not depend on it.
+ * What the kernels read there cannot be checked on the host: a sequence whose
+ * offsets do not lie in 0..T, whose length is negative or above max_pages *
+ * page_tokens, or (bitnet_kv_append) below its new rows is left alone, and a
+ * page number outside 0..num_pages - 1 is not followed (nothing is written
+ * there; its tokens are not seen).  Either records BITNET_ERR_RANGE in the
+ * device status word.
+ * ---------------------------------------------------------------------- */
+typedef struct bitnet_kv_cache {
+  int8_t *k_codes;
+  int8_t *v_codes;
+  float *k_scales;
+  float *v_scales;
+  int64_t num_pages;
+  int32_t heads;
+  int32_t page_tokens;
+  int32_t head_dim;
+} bitnet_kv_cache;
+
+/* Writes the new keys and values of the batch into the cache.
+ *   K, V     [T][heads][head_dim] fp32 or bf16 (dtype), finite, 16-byte
+ *            aligned; token t begins at K + t * k_stride (in elements, rows
+ *            16-byte aligned), so columns of a fused projection's output can
+ *            be given as they are.
+ * For each page and head that receives rows: a = max |x| over its new rows,
+ * d = max(the page's scale if it already holds rows of the sequence, a / 127),
+ * 0 if below 2^-60; new codes are clamp(round_half_away(x * (1 / d)), -127,
+ * 127) (0 for d = 0), and where d grew over the older rows' scale the page's
+ * other codes become round_half_away(code * (d_old * (1 / d))).  All in fp32,
+ * every operation rounded. */
+bitnet_status bitnet_kv_append(const bitnet_kv_cache *cache, const void *K, int64_t k_stride, const void *V,
+                               int64_t v_stride, bitnet_dtype dtype, int64_t T, const int32_t *pages,
+                               int64_t max_pages, const int32_t *lens, const int32_t *offsets, int64_t B,
+                               int64_t max_new, bitnet_stream_t stream);
+
+/* Attention of the new tokens' queries over the cache (which already holds
+ * the new tokens): row t, head i attends with key/value head
+ * i / (q_heads / heads) to the positions j <= its own, and with window > 0 to
+ * the last `window` of them only:
+ *   o = sum_j e^(scale * q.k_j) v_j / sum_j e^(scale * q.k_j).
+ *   Q, O     [T][q_heads][head_dim] of dtype fp32 or bf16, 16-byte aligned,
+ *            not overlapping; q_heads a multiple of cache->heads, at most 32767.
+ * A row that sees nothing (a sequence of length 0, a negative position) is
+ * zeros.  Rows of no sequence are left as they are.  Scores, weights and sums
+ * are fp32; the products run on the tensor cores in fp16, which holds the
+ * codes exactly, q exactly (bf16) or to 22 bits (fp32) and a weight to 11
+ * bits (bf16 Q) or 22 (fp32 Q).
+ *   workspace at least bitnet_kv_attention_workspace_size(...) bytes, 256-byte
+ *            aligned (NULL when that is 0); contents on entry don't matter.
+ *            Calls that may run at the same time need one each. */
+size_t bitnet_kv_attention_workspace_size(const bitnet_kv_cache *cache, bitnet_dtype dtype, int64_t T,
+                                          int32_t q_heads, int64_t B, int64_t max_pages, int64_t max_new,
+                                          int64_t window);
+bitnet_status bitnet_kv_attention(const bitnet_kv_cache *cache, const void *Q, void *O, bitnet_dtype dtype,
+                                  int64_t T, int32_t q_heads, const int32_t *pages, int64_t max_pages,
+                                  const int32_t *lens, const int32_t *offsets, int64_t B, int64_t max_new,
+                                  float scale, int64_t window, void *workspace, size_t workspace_bytes,
+                                  bitnet_stream_t stream);
+
+/* ----------------------------------------------------------------------
+ * Products with 4-bit weights and a scale per group of weights, for layers
+ * that are not ternary (the output head).
+ *   W        [N][K] fp32 or bf16, finite; K a multiple of `group` (32, 64 or
+ *            128), at most 2^24.
+ *   packed   [N][K / 2] bytes, 16-byte aligned: a little-endian 32-bit word
+ *            holds 8 consecutive weights of a row, weight 2i + h of them as
+ *            code + 8 at bits [16h + 4i, 16h + 4i + 4).
+ *   scales   [N][K / group] bf16, 4-byte aligned.
+ * Quantiser: s = bf16(max |w| / 7) of the group (0 if below 2^-60),
+ * code = clamp(round_half_away(w * (1 / s)), -8, 7) (0 for s = 0); weight =
+ * code * s.
+ * ---------------------------------------------------------------------- */
+bitnet_status bitnet_quantize_weights_w4(const void *W, bitnet_dtype w_dtype, int64_t N, int64_t K,
+                                         int32_t group, uint8_t *packed, void *scales, bitnet_stream_t stream);
+
+/* Y [M][N] = X [M][K] times the transpose of those weights; X and Y fp32 or
+ * bf16 each, 16-byte aligned, not overlapping.  Codes are exact, sums fp32.
+ * fp32 X runs as three bf16 terms (24 bits; values of bf16's exponent range)
+ * and needs a workspace of bitnet_w4a16_matmul_workspace_size bytes (256-byte
+ * aligned; 0 for bf16 X).  flags: 0 or BITNET_FLAG_WEIGHTS_STATIC (packed and
+ * scales are not written by the kernel before this call).  Made for few
+ * tokens; more run in blocks that read the weights again. */
+size_t bitnet_w4a16_matmul_workspace_size(int64_t M, int64_t N, int64_t K, bitnet_dtype x_dtype);
+bitnet_status bitnet_w4a16_matmul(const void *X, bitnet_dtype x_dtype, const uint8_t *packed,
+                                  const void *scales, int64_t M, int64_t N, int64_t K, int32_t group, void *Y,
+                                  bitnet_dtype y_dtype, void *workspace, size_t workspace_bytes, uint32_t flags,
+                                  bitnet_stream_t stream);
+
+/* ----------------------------------------------------------------------
+ * Log probabilities from logits.
+ *   logits   [M] rows of V fp32 or bf16 values, row m at logits + m * stride
+ *            (elements; any alignment of the type).
+ *   tokens   [M] int64: logprob[m] = ln p(tokens[m]); a negative token asks
+ *            for none and gives 0; one >= V gives NaN and records
+ *            BITNET_ERR_RANGE.
+ *   entropy  [M]: -sum p ln p.
+ *   top_ids, top_logprobs  [M][top]: the `top` most probable tokens and
+ *            their log probabilities, in falling order, equal logits by the
+ *            lower id first; top <= V and <= BITNET_LOGPROBS_MAX_TOP, 0 for
+ *            none (the arrays may then be NULL).
+ * -infinity is a probability of 0.  A row of nothing else has log
+ * probabilities of -infinity and entropy 0.  A row with a NaN or +infinity
+ * has NaN in all of them.  Sums are fp32, the maximum taken away first.
+ * ---------------------------------------------------------------------- */
+#define BITNET_LOGPROBS_MAX_TOP 32
+bitnet_status bitnet_token_logprobs(const void *logits, bitnet_dtype dtype, int64_t M, int64_t V, int64_t stride,
+                                    const int64_t *tokens, int32_t top, float *logprob, float *entropy,
+                                    int64_t *top_ids, float *top_logprobs, bitnet_stream_t stream);
+
+/* ----------------------------------------------------------------------
  * Status and diagnostics.
  * ---------------------------------------------------------------------- */
 /* Static English text for a status code (never NULL). */
@@ -430,7 +564,8 @@ const char *bitnet_status_string(bitnet_status status);
 
 /* Synchronises `stream`, then reads and clears the device status word of the
  * current device: BITNET_OK, or the first error a kernel recorded
- * (BITNET_ERR_TIMEOUT after a bounded wait gave up). */
+ * (BITNET_ERR_TIMEOUT after a bounded wait gave up, BITNET_ERR_RANGE after a
+ * page, length, offset or token that does not exist). */
 bitnet_status bitnet_get_device_status(bitnet_stream_t stream);
 
 /* ABI version of this header: major * 10000 + minor * 100 + patch.  1.1:

@@ -85,6 +85,26 @@ CHAIN_MAX_STEPS = 256
 _SIGS["bitnet_decode_chain_workspace_size"] = ([C.POINTER(ChainStep), C.c_int], _SZ)
 _SIGS["bitnet_decode_chain"] = ([C.POINTER(ChainStep), C.c_int, _P, _P, _P, _SZ, _P], _ST)
 
+
+class KVCacheStruct(C.Structure):
+    """``bitnet_kv_cache`` of the C header."""
+    _fields_ = [("k_codes", C.c_void_p), ("v_codes", C.c_void_p), ("k_scales", C.c_void_p),
+                ("v_scales", C.c_void_p), ("num_pages", C.c_int64), ("heads", C.c_int32),
+                ("page_tokens", C.c_int32), ("head_dim", C.c_int32)]
+
+
+LOGPROBS_MAX_TOP = 32
+_I32 = C.c_int32
+_SIGS["bitnet_kv_append"] = ([_P, _P, _I64, _P, _I64, _ST, _I64, _P, _I64, _P, _P, _I64, _I64, _P], _ST)
+_SIGS["bitnet_kv_attention_workspace_size"] = ([_P, _ST, _I64, _I32, _I64, _I64, _I64, _I64], _SZ)
+_SIGS["bitnet_kv_attention"] = ([_P, _P, _P, _ST, _I64, _I32, _P, _I64, _P, _P, _I64, _I64, C.c_float, _I64,
+                                 _P, _SZ, _P], _ST)
+_SIGS["bitnet_quantize_weights_w4"] = ([_P, _ST, _I64, _I64, _I32, _P, _P, _P], _ST)
+_SIGS["bitnet_w4a16_matmul_workspace_size"] = ([_I64, _I64, _I64, _ST], _SZ)
+_SIGS["bitnet_w4a16_matmul"] = ([_P, _ST, _P, _P, _I64, _I64, _I64, _I32, _P, _ST, _P, _SZ, C.c_uint32, _P],
+                                _ST)
+_SIGS["bitnet_token_logprobs"] = ([_P, _ST, _I64, _I64, _I64, _P, _I32, _P, _P, _P, _P, _P], _ST)
+
 for _name, (_args, _res) in _SIGS.items():
     _f = getattr(lib, _name)
     _f.argtypes = _args
@@ -464,3 +484,282 @@ def bitnet_decode_chain(steps, x0: torch.Tensor, workspace: torch.Tensor,
     st = lib.bitnet_decode_chain(arr, len(arr), _ptr(x0), _ptr(y_norm), _ptr(workspace),
                                  workspace.numel(), _stream(stream))
     _check(st, "bitnet_decode_chain")
+
+
+# ---------------------------------------------------------------- decode step: cache, attention, head
+# These entry points run on the device of their tensors, whichever is current,
+# and take `stream` (default: that device's current stream) for the tensors
+# that they allocate as well.
+def _on(stream, *tensors):
+    """Checks that the tensors share a CUDA device; (context to run in or
+    None, raw stream) for a call on them."""
+    dev = tensors[0].device
+    for t in tensors:
+        if t.device != dev:
+            if not t.is_cuda:
+                raise ValueError("tensors must be CUDA tensors (there is no CPU fallback)")
+            raise ValueError(f"tensors are on {dev} and on {t.device}")
+    if not tensors[0].is_cuda:
+        raise ValueError("tensors must be CUDA tensors (there is no CPU fallback)")
+    if stream is None:
+        raw = torch._C._cuda_getCurrentRawStream(dev.index)
+        return (None if dev.index == torch._C._cuda_getDevice() else torch.cuda.device(dev)), raw
+    if stream.device != dev:
+        raise ValueError(f"stream is on {stream.device}, the tensors on {dev}")
+    return torch.cuda.stream(stream), stream.cuda_stream
+
+
+def _within(context, call):
+    if context is None:
+        return call()
+    with context:
+        return call()
+
+
+def _is(t: torch.Tensor, name: str, *dtypes):
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name} must have dtype in {dtypes}, got {t.dtype}")
+
+
+def _dense(t: torch.Tensor, name: str, *dtypes):
+    _is(t, name, *dtypes)
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+
+
+class KVCache:
+    """Key/value cache in 8 bits: ``num_pages`` pages of ``page_tokens``
+    tokens (16, 32, 64 or 128), ``heads`` key/value heads of ``head_dim`` (64
+    or 128); for each page and head int8 codes [page_tokens, head_dim] of the
+    keys and of the values, and a scale of each: value = code * scale.  Which
+    pages a sequence uses, in which order, is the caller's page table."""
+
+    def __init__(self, num_pages: int, page_tokens: int, heads: int, head_dim: int, device="cuda:0"):
+        shape = (num_pages, heads, page_tokens, head_dim)
+        self._take(torch.zeros(shape, dtype=torch.int8, device=device),
+                   torch.zeros(shape, dtype=torch.int8, device=device),
+                   torch.zeros(shape[:2], dtype=torch.float32, device=device),
+                   torch.zeros(shape[:2], dtype=torch.float32, device=device))
+
+    @classmethod
+    def from_tensors(cls, k_codes: torch.Tensor, v_codes: torch.Tensor, k_scales: torch.Tensor,
+                     v_scales: torch.Tensor) -> "KVCache":
+        """A cache over existing tensors (not copied): codes [num_pages, heads,
+        page_tokens, head_dim] int8, scales [num_pages, heads] fp32."""
+        self = cls.__new__(cls)
+        self._take(k_codes, v_codes, k_scales, v_scales)
+        return self
+
+    def _take(self, k_codes, v_codes, k_scales, v_scales):
+        for t, name in ((k_codes, "k_codes"), (v_codes, "v_codes")):
+            _dev(t, name, (torch.int8,))
+        for t, name in ((k_scales, "k_scales"), (v_scales, "v_scales")):
+            _dev(t, name, (torch.float32,))
+        if k_codes.dim() != 4 or v_codes.shape != k_codes.shape:
+            raise ValueError("k_codes and v_codes must be [num_pages, heads, page_tokens, head_dim]")
+        if k_scales.shape != k_codes.shape[:2] or v_scales.shape != k_codes.shape[:2]:
+            raise ValueError("k_scales and v_scales must be [num_pages, heads]")
+        if len({t.device for t in (k_codes, v_codes, k_scales, v_scales)}) != 1:
+            raise ValueError("a cache lies on one device")
+        self.k_codes, self.v_codes, self.k_scales, self.v_scales = k_codes, v_codes, k_scales, v_scales
+        self.num_pages, self.heads, self.page_tokens, self.head_dim = k_codes.shape
+        self._struct = KVCacheStruct(k_codes.data_ptr(), v_codes.data_ptr(), k_scales.data_ptr(),
+                                     v_scales.data_ptr(), *(k_codes.shape[i] for i in (0, 1, 2, 3)))
+        self._ref = C.addressof(self._struct)
+
+
+def _batch(pages, lens, offsets, T, max_new):
+    """Checks the arrays that describe a batch; (B, max_pages, max_new)."""
+    _dense(pages, "pages", torch.int32)
+    _dense(lens, "lens", torch.int32)
+    B = lens.numel()
+    if pages.dim() != 2 or pages.shape[0] != B or lens.dim() != 1:
+        raise ValueError("pages must be [B, max_pages] and lens [B]")
+    if offsets is None:
+        if T != B:
+            raise ValueError(f"{T} rows for {B} sequences: without offsets every sequence has one")
+        return B, pages.shape[1], 1
+    _dense(offsets, "offsets", torch.int32)
+    if offsets.numel() != B + 1:
+        raise ValueError(f"offsets has {offsets.numel()} elements, expected B + 1 = {B + 1}")
+    return B, pages.shape[1], T if max_new is None else int(max_new)
+
+
+def bitnet_kv_append(cache: KVCache, K: torch.Tensor, V: torch.Tensor, pages: torch.Tensor,
+                     lens: torch.Tensor, offsets: torch.Tensor | None = None,
+                     max_new: int | None = None, stream=None) -> None:
+    """Quantises the new tokens' keys and values K, V [T, heads, head_dim]
+    (fp32/bf16; columns of a wider row are taken as they are) into the cache.
+    pages [B, max_pages], lens [B] (the new tokens included) and offsets
+    [B + 1] int32 say where: rows offsets[b] .. offsets[b + 1] - 1 are the
+    last tokens of sequence b; without offsets each sequence has one row.
+    ``max_new``: the most rows of a sequence (default: T)."""
+    T = K.shape[0]
+    _is(K, "K", torch.float32, torch.bfloat16)
+    _is(V, "V", K.dtype)
+    H, D = cache.heads, cache.head_dim
+    if K.shape != (T, H, D) or V.shape != (T, H, D):
+        raise ValueError(f"K and V must be [T, {H}, {D}]")
+    ks, vs = K.stride(), V.stride()
+    if T > 0 and not (ks[2] == vs[2] == 1 and (H == 1 or ks[1] == vs[1] == D)):
+        raise ValueError("the heads of a token must lie one after the other in K and V")
+    B, W, most = _batch(pages, lens, offsets, T, max_new)
+    ctx, raw = _on(stream, cache.k_codes, K, V, pages, lens, *(() if offsets is None else (offsets,)))
+    st = _within(ctx, lambda: lib.bitnet_kv_append(
+        cache._ref, K.data_ptr(), ks[0], V.data_ptr(), vs[0], _DTYPE[K.dtype], T, pages.data_ptr(), W,
+        lens.data_ptr(), None if offsets is None else offsets.data_ptr(), B, most, raw))
+    _check(st, "bitnet_kv_append")
+
+
+@functools.lru_cache(maxsize=1024)
+def _kv_workspace(num_pages, heads, page_tokens, head_dim, dtype, T, q_heads, B, W, most, window):
+    some = KVCacheStruct(256, 256, 256, 256, num_pages, heads, page_tokens, head_dim)
+    return lib.bitnet_kv_attention_workspace_size(C.addressof(some), dtype, T, q_heads, B, W, most, window)
+
+
+def bitnet_kv_attention_workspace_size(cache: KVCache, dtype: torch.dtype, T: int, q_heads: int, B: int,
+                                       max_pages: int, max_new: int = 1, window: int = 0) -> int:
+    return _kv_workspace(cache.num_pages, cache.heads, cache.page_tokens, cache.head_dim, _DTYPE[dtype],
+                         int(T), int(q_heads), int(B), int(max_pages), int(max_new), int(window))
+
+
+def bitnet_kv_attention(cache: KVCache, Q: torch.Tensor, pages: torch.Tensor, lens: torch.Tensor,
+                        offsets: torch.Tensor | None = None, max_new: int | None = None,
+                        scale: float | None = None, window: int = 0, O: torch.Tensor | None = None,
+                        workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Causal attention of the new tokens' queries Q [T, q_heads, head_dim]
+    (fp32/bf16) over the cache, which already holds the new tokens; returns O
+    like Q.  pages, lens, offsets and max_new as in ``bitnet_kv_append``;
+    ``scale`` defaults to head_dim ** -0.5; ``window`` > 0 lets a token see
+    the last ``window`` positions only, its own among them.  Without a
+    ``workspace`` (``bitnet_kv_attention_workspace_size`` bytes) one is
+    allocated.  Rows of no sequence are left as O has them (a new O: as its
+    memory was)."""
+    _dense(Q, "Q", torch.float32, torch.bfloat16)
+    if Q.dim() != 3 or Q.shape[2] != cache.head_dim:
+        raise ValueError(f"Q must be [T, q_heads, {cache.head_dim}]")
+    T, q_heads, D = Q.shape
+    B, W, most = _batch(pages, lens, offsets, T, max_new)
+    ctx, raw = _on(stream, cache.k_codes, Q, pages, lens, *(() if offsets is None else (offsets,)),
+                   *(() if O is None else (O,)), *(() if workspace is None else (workspace,)))
+    if O is not None:
+        _dense(O, "O", Q.dtype)
+        if O.shape != Q.shape:
+            raise ValueError("O must have the shape of Q")
+    need = _kv_workspace(cache.num_pages, cache.heads, cache.page_tokens, D, _DTYPE[Q.dtype], T, q_heads, B,
+                         W, most, int(window))
+
+    def call():
+        out, ws = O, workspace
+        if out is None:
+            out = torch.empty_like(Q)
+        if ws is None and need > 0:
+            ws = torch.empty(need, dtype=torch.uint8, device=Q.device)
+        return lib.bitnet_kv_attention(
+            cache._ref, Q.data_ptr(), out.data_ptr(), _DTYPE[Q.dtype], T, q_heads, pages.data_ptr(), W,
+            lens.data_ptr(), None if offsets is None else offsets.data_ptr(), B, most,
+            D ** -0.5 if scale is None else scale, window, None if ws is None else ws.data_ptr(),
+            0 if ws is None else ws.numel() * ws.element_size(), raw), out
+    st, out = _within(ctx, call)
+    _check(st, "bitnet_kv_attention")
+    return out
+
+
+def bitnet_quantize_weights_w4(W: torch.Tensor, group: int = 128, packed: torch.Tensor | None = None,
+                               scales: torch.Tensor | None = None, stream=None):
+    """W [N, K] fp32/bf16 -> (packed [N, K/2] uint8, scales [N, K/group]
+    bf16): 4-bit codes with a scale per group of 32, 64 or 128 weights."""
+    _dense(W, "W", torch.float32, torch.bfloat16)
+    if group not in (32, 64, 128):
+        raise ValueError(f"group must be 32, 64 or 128, got {group}")
+    N, K = W.shape
+    ctx, raw = _on(stream, W, *(t for t in (packed, scales) if t is not None))
+
+    def call():
+        p = torch.empty((N, K // 2), dtype=torch.uint8, device=W.device) if packed is None else packed
+        s = torch.empty((N, K // group), dtype=torch.bfloat16, device=W.device) if scales is None else scales
+        _dense(p, "packed", torch.uint8)
+        _dense(s, "scales", torch.bfloat16)
+        if p.shape != (N, K // 2) or s.shape != (N, K // group):
+            raise ValueError("packed must be [N, K/2] and scales [N, K/group]")
+        return lib.bitnet_quantize_weights_w4(W.data_ptr(), _DTYPE[W.dtype], N, K, group, p.data_ptr(),
+                                              s.data_ptr(), raw), p, s
+    st, p, s = _within(ctx, call)
+    _check(st, "bitnet_quantize_weights_w4")
+    return p, s
+
+
+def bitnet_w4a16_matmul_workspace_size(M: int, N: int, K: int, x_dtype: torch.dtype) -> int:
+    return lib.bitnet_w4a16_matmul_workspace_size(M, N, K, _DTYPE[x_dtype])
+
+
+def bitnet_w4a16_matmul(X: torch.Tensor, packed: torch.Tensor, scales: torch.Tensor,
+                        out_dtype: torch.dtype = torch.bfloat16, Y: torch.Tensor | None = None,
+                        workspace: torch.Tensor | None = None, weights_static: bool = False,
+                        stream=None) -> torch.Tensor:
+    """Y [M, N] = X [M, K] (fp32/bf16) times the transpose of the 4-bit
+    weights of ``bitnet_quantize_weights_w4``; Y fp32/bf16.  Made for few
+    tokens (a decode step); more run in blocks."""
+    _dense(X, "X", torch.float32, torch.bfloat16)
+    _dense(packed, "packed", torch.uint8)
+    _dense(scales, "scales", torch.bfloat16)
+    M, K = X.shape
+    N = packed.shape[0]
+    if packed.shape[1] * 2 != K:
+        raise ValueError(f"packed has {packed.shape[1]} bytes per row, expected K/2 = {K // 2}")
+    groups = scales.shape[1] if scales.dim() == 2 else 0
+    if groups == 0 or scales.shape[0] != N or K % groups != 0:
+        raise ValueError("scales must be [N, K/group]")
+    ctx, raw = _on(stream, X, packed, scales, *(t for t in (Y, workspace) if t is not None))
+    if Y is not None:
+        _dense(Y, "Y", torch.float32, torch.bfloat16)
+        if Y.shape != (M, N):
+            raise ValueError(f"Y must be [{M}, {N}]")
+
+    def call():
+        out, ws = Y, workspace
+        if out is None:
+            out = torch.empty((M, N), dtype=out_dtype, device=X.device)
+            _is(out, "out_dtype", torch.float32, torch.bfloat16)
+        if ws is None:
+            need = lib.bitnet_w4a16_matmul_workspace_size(M, N, K, _DTYPE[X.dtype])
+            if need > 0:
+                ws = torch.empty(need, dtype=torch.uint8, device=X.device)
+        return lib.bitnet_w4a16_matmul(
+            X.data_ptr(), _DTYPE[X.dtype], packed.data_ptr(), scales.data_ptr(), M, N, K, K // groups,
+            out.data_ptr(), _DTYPE[out.dtype], None if ws is None else ws.data_ptr(),
+            0 if ws is None else ws.numel() * ws.element_size(),
+            FLAG_WEIGHTS_STATIC if weights_static else 0, raw), out
+    st, out = _within(ctx, call)
+    _check(st, "bitnet_w4a16_matmul")
+    return out
+
+
+def bitnet_token_logprobs(logits: torch.Tensor, tokens: torch.Tensor, top: int = 0, stream=None):
+    """For each row of logits [M, V] (fp32/bf16; rows may be part of wider
+    ones): (logprob [M] of tokens[m], entropy [M], top_ids [M, top] int64,
+    top_logprobs [M, top]), all but the ids fp32.  tokens [M] int64; a
+    negative one asks for no log probability (0).  ``top`` <= 32 alternatives
+    come most probable first, equal ones by the lower id."""
+    _is(logits, "logits", torch.float32, torch.bfloat16)
+    _dense(tokens, "tokens", torch.int64)
+    M, V = logits.shape
+    if tokens.shape != (M,):
+        raise ValueError(f"tokens must be [{M}]")
+    if V > 1 and logits.stride(1) != 1:
+        raise ValueError("the values of a row of logits must be contiguous")
+    ctx, raw = _on(stream, logits, tokens)
+
+    def call():
+        dev = logits.device
+        lp = torch.empty((2, M), dtype=torch.float32, device=dev)
+        ids = torch.empty((M, max(top, 0)), dtype=torch.int64, device=dev)
+        tl = torch.empty((M, max(top, 0)), dtype=torch.float32, device=dev)
+        at = lp.data_ptr()
+        return lib.bitnet_token_logprobs(
+            logits.data_ptr(), _DTYPE[logits.dtype], M, V, logits.stride(0), tokens.data_ptr(), top, at,
+            at + 4 * M, ids.data_ptr() if top > 0 else None, tl.data_ptr() if top > 0 else None,
+            raw), (lp[0], lp[1], ids, tl)
+    st, out = _within(ctx, call)
+    _check(st, "bitnet_token_logprobs")
+    return out

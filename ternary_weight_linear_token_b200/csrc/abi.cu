@@ -60,6 +60,7 @@ bitnet_status device_ctx(bitnet_stream_t stream, LaunchCtx *ctx) {
   ctx->stream = reinterpret_cast<cudaStream_t>(stream);
   ctx->status = d.status;
   ctx->num_sms = d.num_sms;
+  ctx->device = dev;
   ctx->pdl = true;
   return BITNET_OK;
 }
@@ -281,6 +282,9 @@ int matmul_args_status(const void *X, int x_dtype, const float *s, const uint8_t
                       static_cast<bitnet_epilogue>(epi), Y, static_cast<bitnet_dtype>(y_dtype),
                       nullptr, 0, flags, false, false);
 }
+
+// The launch context of the current device, for the other C-ABI files.
+int launch_ctx_status(bitnet_stream_t stream, LaunchCtx *ctx) { return device_ctx(stream, ctx); }
 
 }  // namespace bitnet
 

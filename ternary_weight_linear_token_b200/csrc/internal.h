@@ -6,6 +6,8 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include <atomic>
+
 namespace bitnet {
 
 // Element kinds used by the kernels (mirror bitnet_dtype values).
@@ -15,6 +17,7 @@ struct LaunchCtx {
   cudaStream_t stream;
   int *status;      // device status word of the current device
   int num_sms;
+  int device;       // its number, below 64
   bool pdl;         // launch with programmatic stream serialization
 };
 
@@ -142,6 +145,65 @@ int matmul_args_status(const void *X, int x_dtype, const float *s, const uint8_t
                        const float *gamma, int64_t M, int64_t N, int64_t K, int epi,
                        const void *Y, int y_dtype, uint32_t flags);
 
+// abi.cu: the launch context (stream, status word, SM count) of the current
+// device, as a bitnet_status value (0 = OK).
+int launch_ctx_status(struct CUstream_st *stream, LaunchCtx *ctx);
+
+// The 8-bit key/value cache as the kernels see it (bitnet_kv_cache): codes
+// [pages][heads][page_tokens][head_dim], scales [pages][heads], value =
+// code * scale.
+struct KvCache {
+  int8_t *k_codes, *v_codes;
+  float *k_scales, *v_scales;
+  int64_t pages;
+  int heads, page_tokens, head_dim;
+};
+// The sequences of a call: row t of the new tokens belongs to sequence b when
+// offsets[b] <= t < offsets[b + 1] (offsets null: row b to sequence b); the
+// last of them sits at position lens[b] - 1 of its sequence, and position p
+// in row p % page_tokens of page pages[b][p / page_tokens].
+struct KvBatch {
+  const int *pages, *lens, *offsets;
+  int64_t max_pages, B, T;
+};
+
+// A scale is 0 or at least this (2^-60): the attention kernels add its
+// logarithm to the scores, which must stay inside the exponent range.
+constexpr float kKvMinScale = 8.673617379884035e-19f;
+
+// kv_append.cu
+cudaError_t launch_kv_append(const KvCache &cache, const void *K, const void *V, int kind,
+                             int64_t k_stride, int64_t v_stride, const KvBatch &batch,
+                             int64_t max_new, const LaunchCtx &ctx);
+
+// kv_attention.cu: Q, O [T][q_heads][head_dim] fp32 or bf16.
+struct AttnArgs {
+  const void *Q;
+  void *O;
+  int kind, q_heads;
+  float scale;
+  int64_t window;   // 0: none
+  int64_t max_new;
+};
+size_t kv_attention_workspace(const KvCache &cache, const KvBatch &batch, const AttnArgs &args);
+bool kv_attention_fits(const KvCache &cache, const KvBatch &batch, const AttnArgs &args);
+cudaError_t launch_kv_attention(const KvCache &cache, const KvBatch &batch, const AttnArgs &args,
+                                void *workspace, const LaunchCtx &ctx);
+
+// gemv_w4.cu: 4-bit weights [N][K / 2] with bf16 scales [N][K / group].
+cudaError_t launch_quantize_weights_w4(const void *W, int w_kind, int64_t N, int64_t K, int group,
+                                       uint8_t *packed, uint16_t *scales, const LaunchCtx &ctx);
+size_t w4_workspace(int64_t M, int64_t N, int64_t K, int x_kind);
+cudaError_t launch_w4(const void *X, int x_kind, const uint8_t *packed, const uint16_t *scales,
+                      int64_t M, int64_t N, int64_t K, int group, void *Y, int y_kind,
+                      void *workspace, bool weights_static, const LaunchCtx &ctx);
+
+// token_logprobs.cu
+constexpr int kLogprobsMaxTop = 32;
+cudaError_t launch_token_logprobs(const void *X, int x_kind, int64_t M, int64_t V, int64_t stride,
+                                  const int64_t *tokens, int top, float *logprob, float *entropy,
+                                  int64_t *top_ids, float *top_logprobs, const LaunchCtx &ctx);
+
 // Launch helper: cudaLaunchKernelEx with the PDL attribute when ctx.pdl.
 template <typename... KArgs, typename... Args>
 cudaError_t launch_k(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem,
@@ -179,6 +241,18 @@ cudaError_t launch_k_cluster(void (*kernel)(KArgs...), dim3 grid, dim3 block, si
   cfg.attrs = attr;
   cfg.numAttrs = ctx.pdl ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, kernel, static_cast<KArgs>(args)...);
+}
+
+// Allows a kernel its dynamic shared memory, once per device (`ready`: a bit
+// for each).
+template <typename K>
+cudaError_t allow_smem(K kernel, size_t bytes, std::atomic<uint64_t> &ready, const LaunchCtx &ctx) {
+  const uint64_t bit = uint64_t(1) << ctx.device;
+  if ((ready.load(std::memory_order_acquire) & bit) != 0) return cudaSuccess;
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             static_cast<int>(bytes));
+  if (e == cudaSuccess) ready.fetch_or(bit, std::memory_order_release);
+  return e;
 }
 
 inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }

@@ -1,0 +1,725 @@
+// kv_attention.cu -- attention over the 8-bit paged key/value cache.
+//
+// For a query row q (one query token and head) at position pos of its
+// sequence, over the visible positions j <= pos (and j > pos - window):
+//   s_j = scale * (q . kc_j) * ks(j),  o = sum_j e^{s_j} vs(j) vc_j / sum_j e^{s_j}
+// with int8 codes kc, vc and one scale ks, vs per page and head.
+//
+// The int8 codes are exact in fp16, so the tensor cores multiply them
+// (mma m16n8k16, fp32 sums) after a byte permute and one subtraction per two
+// codes: the permute puts (code + 128) under the fp16 exponent of 1024, the
+// subtraction takes 1152 away.  The tokens are the M axis (16 at a time, all
+// in one page) and the query rows the N axis, so a decode step of 4 to 8
+// query heads per key head fills a tile of 8 rows:
+//   S^T = Kc Q^T            the codes of a thread's 16-byte loads are its A
+//                           fragments (the order of the K axis is free)
+//   O^T += Vc^T P^T         S^T's accumulators become P^T's B fragments by
+//                           one 8 x 8 transpose
+// q is scaled by a power of two per row so that fp16 holds it: bf16 values
+// exactly, fp32 ones as a sum of two halves (22 bits), which take two
+// neighbouring columns of the tile; fp32 P is split the same way.
+// vs enters as log2(vs) added to the score: p' = 2^(s + log2 vs - m) with the
+// running maximum m of that sum, so O += p' vc needs no further scale, while
+// the row sum adds p' / vs.  A page of zeros (vs = 0) counts with log2 vs =
+// -60.  p' is held 2^kRaise higher, and m may lag behind by kLazy: p' stays
+// below 2^15, and fp16 rounds it by at most 2^-12 of itself or, below fp16's
+// normal numbers, by 2^-25: 2^-32 of the largest weight.
+//
+// A CTA's 4 warps take every 4th chunk of 32 tokens of its piece of the
+// sequence, each with its own ring of chunks filled by bulk copies (K and V
+// of a chunk are contiguous in a page), page numbers and scales fetched
+// ahead; they join their sums in shared memory.  Few rows over a long cache
+// are cut into pieces, which a second kernel joins in piece order.
+#include <cuda_fp16.h>
+
+#include <atomic>
+
+#include "common.cuh"
+#include "internal.h"
+
+namespace bitnet {
+namespace {
+
+constexpr int kStatusRange = 6;  // == BITNET_ERR_RANGE
+constexpr int kWarps = 4;
+constexpr int kChunk = 32;       // tokens per ring stage
+constexpr float kLazy = 8.0f;    // the maximum follows the scores once they pass it by this (log2)
+constexpr float kRaise = 7.0f;
+constexpr float kLog2e = 1.4426950408889634f;
+
+struct AttnParams {
+  KvCache cache;
+  KvBatch batch;
+  const void *q;
+  void *o;
+  int q_heads, group;
+  float scale_log2;
+  int64_t window;
+  int row_tiles, pieces;
+  int64_t piece;       // tokens per piece, a multiple of kChunk
+  float *part_o;       // [pieces][T * q_heads][D]; null: one piece, O written here
+  float2 *part_ml;     // [pieces][T * q_heads] (max, sum)
+  int *status;
+};
+
+template <int D> struct Ring {
+  static constexpr int kStages = D == 128 ? 3 : 6;
+  static constexpr int kBytes = kChunk * D;            // K, and V, of a chunk
+  static constexpr int kStageBytes = 2 * kBytes;
+};
+// per warp and stage: ks, log2 vs, 1 / vs of the chunk's two 16-token tiles
+struct ChunkScales {
+  float ks[2], lv[2], iv[2];
+};
+template <int D> constexpr size_t attn_smem() {
+  return static_cast<size_t>(kWarps) * Ring<D>::kStages *
+         (Ring<D>::kStageBytes + sizeof(ChunkScales) + sizeof(uint64_t));
+}
+
+// The rows of sequence b and its length; false (and `bad` set) for numbers
+// that do not describe one.
+__device__ __forceinline__ bool sequence(const KvBatch &batch, int P, int64_t b, int64_t *r0,
+                                         int64_t *r1, int64_t *len) {
+  *len = batch.lens[b];
+  *r0 = b;
+  *r1 = b + 1;
+  if (batch.offsets != nullptr) {
+    *r0 = batch.offsets[b];
+    *r1 = batch.offsets[b + 1];
+  }
+  return *r0 >= 0 && *r1 <= batch.T && *r0 <= *r1 && *len >= 0 && *len <= batch.max_pages * P;
+}
+
+// Positions that some of the queries i0..i1 of a sequence sees: [lo, hi),
+// lo rounded down to a chunk.
+__device__ __forceinline__ void visible(int64_t len, int64_t n, int64_t i0, int64_t i1,
+                                        int64_t window, int64_t *lo, int64_t *hi) {
+  *hi = len - n + i1 + 1;
+  const int64_t first = window > 0 ? len - n + i0 - window + 1 : 0;
+  *lo = (first > 0 ? first : 0) / kChunk * kChunk;
+}
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                        uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// Transpose of an 8 x 8 matrix of halves held two per lane.
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+
+__device__ __forceinline__ uint32_t half2_bits(__half2 h) {
+  return *reinterpret_cast<uint32_t *>(&h);
+}
+// Two codes + 128, one in the low byte of each half, to two halves.
+__device__ __forceinline__ uint32_t from_biased(uint32_t x) {
+  const uint32_t bias = 0x64806480u;  // 1152, twice
+  return half2_bits(__hsub2(*reinterpret_cast<__half2 *>(&x), *reinterpret_cast<const __half2 *>(&bias)));
+}
+// Bytes 0, 1 (2, 3) of w (codes + 128) as two halves.
+__device__ __forceinline__ uint32_t codes01(uint32_t w) { return from_biased(__byte_perm(w, 0x64646464u, 0x4140)); }
+__device__ __forceinline__ uint32_t codes23(uint32_t w) { return from_biased(__byte_perm(w, 0x64646464u, 0x4342)); }
+
+template <typename T> __device__ __forceinline__ T lds(const void *p) { return *static_cast<const T *>(p); }
+
+// One row tile of one piece.  TERMS: columns per query row (1 bf16, 2 fp32);
+// NT: column tiles of 8.
+template <int D, int TERMS, int NT>
+__device__ __forceinline__ void attend(const AttnParams &p, uint8_t *smem, int64_t b, int h,
+                                       int row_tile, int64_t piece_index, int64_t r0, int64_t n,
+                                       int64_t len, uint32_t &phase) {
+  using R = Ring<D>;
+  constexpr int kRows = 8 * NT / TERMS;
+  constexpr int kSteps = D / 16;     // K steps of S^T; M tiles of O^T
+  constexpr int kPer = 2 / TERMS;    // query rows per lane and column tile
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  const int P = p.cache.page_tokens, H = p.cache.heads, G = p.group;
+  uint8_t *ring = smem + warp * R::kStages * R::kStageBytes;
+  ChunkScales *scales = reinterpret_cast<ChunkScales *>(smem + kWarps * R::kStages * R::kStageBytes) +
+                        warp * R::kStages;
+  uint64_t *full = reinterpret_cast<uint64_t *>(
+                       smem + kWarps * R::kStages * (R::kStageBytes + sizeof(ChunkScales))) +
+                   warp * R::kStages;
+
+  // query rows of the tile: row = query * G + head of the group
+  const int64_t row0 = static_cast<int64_t>(row_tile) * kRows;
+  const int64_t rows = n * G - row0 < kRows ? n * G - row0 : kRows;
+  int64_t lo, hi;
+  visible(len, n, row0 / G, (row0 + rows - 1) / G, p.window, &lo, &hi);
+  lo += piece_index * p.piece;
+  if (hi > lo + p.piece) hi = lo + p.piece;
+  const int64_t chunks = hi > lo ? (hi - lo + kChunk - 1) / kChunk : 0;
+  if (chunks == 0 && p.part_o != nullptr) return;  // the joining kernel knows
+
+  // The page of a lane's tile of the chunk (lanes 0-3: tile = lane & 1, K or
+  // V = lane >> 1); -1 where there is none.
+  const int *table = p.batch.pages + b * p.batch.max_pages;
+  auto page_of = [&](int64_t c) -> int {
+    const int64_t tok = lo + c * kChunk + 16 * (lane & 1);
+    return (lane < 4 && c < chunks && tok < hi) ? __ldg(table + tok / P) : -1;
+  };
+  auto good_page = [&](int page, int64_t c) -> bool {
+    const int64_t tok = lo + c * kChunk + 16 * (lane & 1);
+    if (lane >= 4 || c >= chunks || tok >= hi) return false;
+    if (page >= 0 && page < p.cache.pages) return true;
+    record_status(p.status, kStatusRange);
+    return false;
+  };
+  // Lanes 0-3 copy their tile (pages of 32 tokens and more: the chunk's first
+  // lane copies both tiles' bytes).
+  auto issue = [&](int64_t c, int page) -> float {
+    const int st = static_cast<int>((c / kWarps) % R::kStages);
+    const bool ok = good_page(page, c);
+    const int64_t tok = lo + c * kChunk + 16 * (lane & 1);
+    const unsigned pair = __ballot_sync(0xffffffffu, ok);
+    const bool whole = P >= kChunk;  // both tiles in one page
+    const uint32_t bytes = whole ? R::kBytes : R::kBytes / 2;
+    const unsigned copies = whole ? pair & 5u : pair & 15u;
+    if (lane == 0) mbar_arrive_expect_tx(&full[st], bytes * __popc(copies));
+    __syncwarp();
+    float s = -1.0f;  // no page
+    if (ok) {
+      const int64_t head = static_cast<int64_t>(page) * H + h;
+      s = __ldg((lane >> 1 ? p.cache.v_scales : p.cache.k_scales) + head);
+      if ((copies >> lane) & 1u) {
+        const int8_t *src = (lane >> 1 ? p.cache.v_codes : p.cache.k_codes) + (head * P + tok % P) * D;
+        bulk_g2s(ring + st * R::kStageBytes + (lane >> 1) * R::kBytes + (lane & 1) * (R::kBytes / 2),
+                 src, bytes, &full[st]);
+      }
+    }
+    return s;
+  };
+  auto keep_scale = [&](int64_t c, float s) {
+    ChunkScales &k = scales[(c / kWarps) % R::kStages];
+    if (lane < 2) k.ks[lane] = s;
+    if (lane == 2 || lane == 3) {
+      // s = 0: a page of zeros; s < 0: no page, its tokens are not seen
+      const bool some = !(s < kKvMinScale);
+      k.lv[lane & 1] = some ? log2f(s) : -60.0f;
+      k.iv[lane & 1] = some ? __fdiv_rn(1.0f, s) : 1.152921504606846976e18f;  // 2^60
+    }
+  };
+
+  // ring: the first kStages chunks of this warp
+  int next_page = page_of(warp);
+  for (int i = 0; i < R::kStages; ++i) {
+    const int64_t c = warp + static_cast<int64_t>(i) * kWarps;
+    if (c >= chunks) break;
+    const int page = next_page;
+    next_page = page_of(c + kWarps);
+    keep_scale(c, issue(c, page));
+  }
+
+  // q as B fragments: column g of column tile j is row j * 8 / TERMS + g / TERMS
+  uint32_t qf[NT][kSteps][2];
+  float fac[NT][kPer];     // score factor of the lane's rows (columns 2t, 2t + 1)
+  int64_t pos[NT][kPer];   // their positions; -1: no such row
+#pragma unroll
+  for (int j = 0; j < NT; ++j) {
+    const int64_t row = row0 + j * (8 / TERMS) + g / TERMS;
+    const bool have = row < row0 + rows;
+    const int64_t at = ((r0 + row / G) * p.q_heads + static_cast<int64_t>(h) * G + row % G) * D;
+    float v[D / 4];
+    float peak = 0.0f;
+#pragma unroll
+    for (int c = 0; c < D / 64; ++c)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        float x[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        if (have) {
+          const int64_t e = at + 64 * c + 16 * t + 4 * i;
+          if (TERMS == 2) {
+            const float4 f = __ldg(reinterpret_cast<const float4 *>(static_cast<const float *>(p.q) + e));
+            x[0] = f.x; x[1] = f.y; x[2] = f.z; x[3] = f.w;
+          } else {
+            const uint2 u = __ldg(reinterpret_cast<const uint2 *>(static_cast<const __nv_bfloat16 *>(p.q) + e));
+            x[0] = __uint_as_float(u.x << 16); x[1] = __uint_as_float(u.x & 0xFFFF0000u);
+            x[2] = __uint_as_float(u.y << 16); x[3] = __uint_as_float(u.y & 0xFFFF0000u);
+          }
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          v[(c * 4 + i) * 4 + e] = x[e];
+          peak = fmaxf(peak, fabsf(x[e]));
+        }
+      }
+    peak = fmaxf(peak, __shfl_xor_sync(0xffffffffu, peak, 1));
+    peak = fmaxf(peak, __shfl_xor_sync(0xffffffffu, peak, 2));
+    // 2^k brings the row's largest value into [2^14, 2^15)
+    int k = 14 - (static_cast<int>(__float_as_uint(peak) >> 23) - 127);
+    k = k < -110 ? -110 : (k > 110 ? 110 : k);
+    const float up = __uint_as_float(static_cast<uint32_t>(127 + k) << 23);
+    const float f = __fmul_rn(p.scale_log2, __uint_as_float(static_cast<uint32_t>(127 - k) << 23));
+#pragma unroll
+    for (int s = 0; s < kSteps; ++s)
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        const float a = __fmul_rn(v[s * 4 + 2 * r], up), c = __fmul_rn(v[s * 4 + 2 * r + 1], up);
+        __half2 x = __floats2half2_rn(a, c);
+        if (TERMS == 2 && (g & 1) != 0) {
+          const float2 hi2 = __half22float2(x);
+          x = __floats2half2_rn(__fsub_rn(a, hi2.x), __fsub_rn(c, hi2.y));
+        }
+        qf[j][s][r] = half2_bits(x);
+      }
+#pragma unroll
+    for (int r = 0; r < kPer; ++r) {
+      const int col = 2 * t + r;
+      fac[j][r] = __shfl_sync(0xffffffffu, f, col * 4);
+      const int64_t mine = row0 + j * (8 / TERMS) + col / TERMS;
+      pos[j][r] = mine < row0 + rows ? len - n + mine / G : -1;
+    }
+  }
+
+  float acc[NT][kSteps][4];
+  float m[NT][kPer], l[NT][kPer];
+#pragma unroll
+  for (int j = 0; j < NT; ++j) {
+#pragma unroll
+    for (int s = 0; s < kSteps; ++s)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) acc[j][s][e] = 0.0f;
+#pragma unroll
+    for (int r = 0; r < kPer; ++r) {
+      m[j][r] = -INFINITY;
+      l[j][r] = 0.0f;
+    }
+  }
+  // positions that every row of the tile sees need no mask
+  // (columns past the last row hold zeros and are not stored)
+  const int64_t all_hi = len - n + row0 / G + 1;
+  const int64_t all_lo = p.window > 0 ? len - n + (row0 + rows - 1) / G - p.window + 1 : 0;
+
+  __syncwarp();
+  for (int64_t c = warp; c < chunks; c += kWarps) {
+    const int st = static_cast<int>((c / kWarps) % R::kStages);
+    const bool ok = mbar_wait(&full[st], (phase >> st) & 1u, p.status);
+    if (!__all_sync(0xffffffffu, ok)) break;
+    phase ^= 1u << st;
+    const uint8_t *kt = ring + st * R::kStageBytes;
+    const uint8_t *vt = kt + R::kBytes;
+    const int64_t tok0 = lo + c * kChunk;
+
+    // ---- scores (log2) of the chunk's two tiles: [tile][j][row of lane][token g, g + 8]
+    float s2[2][NT][kPer][2];
+#pragma unroll
+    for (int tile = 0; tile < 2; ++tile) {
+      float sc[NT][4];
+#pragma unroll
+      for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) sc[j][e] = 0.0f;
+#pragma unroll
+      for (int q = 0; q < D / 64; ++q) {
+        const uint4 a = lds<uint4>(kt + (tile * 16 + g) * D + 64 * q + 16 * t);
+        const uint4 a8 = lds<uint4>(kt + (tile * 16 + g + 8) * D + 64 * q + 16 * t);
+        const uint32_t w[4] = {a.x, a.y, a.z, a.w}, w8[4] = {a8.x, a8.y, a8.z, a8.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t u = w[i] ^ 0x80808080u, u8 = w8[i] ^ 0x80808080u;
+          const uint32_t a0 = codes01(u), a1 = codes01(u8), a2 = codes23(u), a3 = codes23(u8);
+#pragma unroll
+          for (int j = 0; j < NT; ++j)
+            mma_f16(sc[j], a0, a1, a2, a3, qf[j][q * 4 + i][0], qf[j][q * 4 + i][1]);
+        }
+      }
+      const float ks = scales[st].ks[tile], lv = scales[st].lv[tile];
+      const int64_t tok = tok0 + 16 * tile;
+      const bool masked = tok + 16 > all_hi || tok < all_lo || tok + 16 > hi || ks < 0.0f;
+#pragma unroll
+      for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int r = 0; r < kPer; ++r)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const float x = TERMS == 2 ? sc[j][2 * e] + sc[j][2 * e + 1] : sc[j][2 * e + r];
+            float y = __fmaf_rn(x, ks * fac[j][r], lv);
+            if (masked) {
+              const int64_t at = tok + g + 8 * e;
+              const bool seen = ks >= 0.0f && at <= pos[j][r] && at < hi && (p.window <= 0 || at > pos[j][r] - p.window);
+              if (!seen) y = -INFINITY;
+            }
+            s2[tile][j][r][e] = y;
+          }
+    }
+
+    // ---- running maximum
+    bool grow = false;
+    float top[NT][kPer];
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+#pragma unroll
+      for (int r = 0; r < kPer; ++r) {
+        float x = fmaxf(fmaxf(s2[0][j][r][0], s2[0][j][r][1]), fmaxf(s2[1][j][r][0], s2[1][j][r][1]));
+        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+        top[j][r] = x;
+        grow |= x > m[j][r] + kLazy;  // also the first finite score (m = -inf)
+      }
+    if (__any_sync(0xffffffffu, grow)) {
+#pragma unroll
+      for (int j = 0; j < NT; ++j) {
+        float f[kPer];
+#pragma unroll
+        for (int r = 0; r < kPer; ++r) {
+          const float to = fmaxf(m[j][r], top[j][r]);
+          f[r] = m[j][r] == to ? 1.0f : ex2(m[j][r] - to);
+          m[j][r] = to;
+          l[j][r] *= f[r];
+        }
+#pragma unroll
+        for (int s = 0; s < kSteps; ++s)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) acc[j][s][e] *= f[(e & 1) % kPer];
+      }
+    }
+
+    // ---- weights, row sums and O^T
+    float from[NT][kPer];
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+#pragma unroll
+      for (int r = 0; r < kPer; ++r) from[j][r] = m[j][r] == -INFINITY ? 0.0f : m[j][r] - kRaise;
+#pragma unroll
+    for (int tile = 0; tile < 2; ++tile) {
+      const float iv = scales[st].iv[tile];
+      uint32_t pf[NT][2];
+#pragma unroll
+      for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          __half2 x;
+          if (TERMS == 2) {
+            const float a = ex2(s2[tile][j][0][e] - from[j][0]);
+            l[j][0] = __fmaf_rn(a, iv, l[j][0]);
+            const float hi_part = __half2float(__float2half_rn(a));
+            x = __floats2half2_rn(hi_part, a - hi_part);
+          } else {
+            float a[2];
+#pragma unroll
+            for (int r = 0; r < kPer; ++r) {
+              a[r] = ex2(s2[tile][j][r][e] - from[j][r]);
+              l[j][r] = __fmaf_rn(a[r], iv, l[j][r]);
+            }
+            x = __floats2half2_rn(a[0], a[kPer - 1]);
+          }
+          pf[j][e] = transpose8(half2_bits(x));
+        }
+      constexpr int kWords = D / 32;  // 32-bit words of a lane's columns
+      uint32_t w[4][kWords];          // tokens 2t, 2t + 1, 2t + 8, 2t + 9
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const uint8_t *src = vt + (tile * 16 + 2 * t + (k & 1) + 8 * (k >> 1)) * D + g * (D / 8);
+        if (D == 128) {
+          const uint4 x = lds<uint4>(src);
+          w[k][0] = x.x; w[k][1] = x.y; w[k][kWords - 2] = x.z; w[k][kWords - 1] = x.w;
+        } else {
+          const uint2 x = lds<uint2>(src);
+          w[k][0] = x.x; w[k][1] = x.y;
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < kWords; ++i) {
+        uint32_t x[2][2];  // [token pair][columns 0 1 | 2 3]: bytes col0 a, b, col1 a, b
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          const uint32_t a = w[2 * q][i] ^ 0x80808080u, c2 = w[2 * q + 1][i] ^ 0x80808080u;
+          x[q][0] = __byte_perm(a, c2, 0x5140);
+          x[q][1] = __byte_perm(a, c2, 0x7362);
+        }
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          const uint32_t a0 = codes01(x[0][q]), a1 = codes23(x[0][q]);
+          const uint32_t a2 = codes01(x[1][q]), a3 = codes23(x[1][q]);
+#pragma unroll
+          for (int j = 0; j < NT; ++j) mma_f16(acc[j][2 * i + q], a0, a1, a2, a3, pf[j][0], pf[j][1]);
+        }
+      }
+    }
+
+    // ---- refill this stage
+    __syncwarp();  // every lane has read it
+    const int64_t nc = c + static_cast<int64_t>(kWarps) * R::kStages;
+    if (nc < chunks) {
+      const int page = next_page;
+      next_page = page_of(nc + kWarps);
+      keep_scale(nc, issue(nc, page));
+      __syncwarp();
+    }
+  }
+
+  // ---- join the warps: [warp][row][D] sums, [warp][row] (m, l)
+#pragma unroll
+  for (int j = 0; j < NT; ++j)
+#pragma unroll
+    for (int r = 0; r < kPer; ++r) {
+      l[j][r] += __shfl_xor_sync(0xffffffffu, l[j][r], 4);
+      l[j][r] += __shfl_xor_sync(0xffffffffu, l[j][r], 8);
+      l[j][r] += __shfl_xor_sync(0xffffffffu, l[j][r], 16);
+    }
+  __syncthreads();  // the rings are idle
+  float *so = reinterpret_cast<float *>(smem);
+  float2 *sml = reinterpret_cast<float2 *>(so + kWarps * kRows * D);
+#pragma unroll
+  for (int j = 0; j < NT; ++j)
+#pragma unroll
+    for (int r = 0; r < kPer; ++r) {
+      const int row = j * (8 / TERMS) + (2 * t + r) / TERMS;
+      if (g == 0) sml[warp * kRows + row] = make_float2(m[j][r], l[j][r]);
+#pragma unroll
+      for (int s = 0; s < kSteps; ++s) {
+        // M tile s: columns d, d + 1 of the head
+        const int d = g * (D / 8) + 2 * s;
+        float2 x;
+        if (TERMS == 2)
+          x = make_float2(acc[j][s][0] + acc[j][s][1], acc[j][s][2] + acc[j][s][3]);
+        else
+          x = make_float2(acc[j][s][r], acc[j][s][2 + r]);
+        *reinterpret_cast<float2 *>(so + (warp * kRows + row) * D + d) = x;
+      }
+    }
+  __syncthreads();
+  for (int i = threadIdx.x; i < kRows * D / 2; i += kWarps * 32) {
+    const int row = i / (D / 2), d = i % (D / 2) * 2;
+    if (row >= rows) break;
+    float top = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) top = fmaxf(top, sml[w * kRows + row].x);
+    float x = 0.0f, y = 0.0f, sum = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      const float2 ml = sml[w * kRows + row];
+      const float f = ml.x == -INFINITY ? 0.0f : ex2(ml.x - top);
+      const float2 v = *reinterpret_cast<const float2 *>(so + (w * kRows + row) * D + d);
+      x = __fmaf_rn(f, v.x, x);
+      y = __fmaf_rn(f, v.y, y);
+      sum = __fmaf_rn(f, ml.y, sum);
+    }
+    const int64_t gr = row0 + row;
+    const int64_t out_row = (r0 + gr / G) * p.q_heads + static_cast<int64_t>(h) * G + gr % G;
+    if (p.part_o != nullptr) {
+      const int64_t at = piece_index * p.batch.T * p.q_heads + out_row;
+      *reinterpret_cast<float2 *>(p.part_o + at * D + d) = make_float2(x, y);
+      if (d == 0) p.part_ml[at] = make_float2(top, sum);
+    } else {
+      const float inv = sum == 0.0f ? 0.0f : __fdiv_rn(1.0f, sum);  // nothing visible: zeros
+      if (TERMS == 2)
+        *reinterpret_cast<float2 *>(static_cast<float *>(p.o) + out_row * D + d) = make_float2(x * inv, y * inv);
+      else
+        *reinterpret_cast<__nv_bfloat162 *>(static_cast<__nv_bfloat16 *>(p.o) + out_row * D + d) =
+            __floats2bfloat162_rn(x * inv, y * inv);
+    }
+  }
+}
+
+template <int D, int TERMS, int NT>
+__global__ void __launch_bounds__(kWarps * 32, 2) kv_attention_kernel(const AttnParams p) {
+  extern __shared__ __align__(128) uint8_t smem[];
+  using R = Ring<D>;
+  uint64_t *full = reinterpret_cast<uint64_t *>(
+      smem + kWarps * R::kStages * (R::kStageBytes + sizeof(ChunkScales)));
+  if (threadIdx.x < kWarps * R::kStages) mbar_init(&full[threadIdx.x], 1);
+  fence_barrier_init();
+  __syncthreads();
+  pdl_wait();
+  pdl_launch_dependents();
+  constexpr int kRows = 8 * NT / TERMS;
+  // piece fastest, then head, row tile, sequence
+  int64_t i = blockIdx.x;
+  const int64_t piece = i % p.pieces;
+  i /= p.pieces;
+  const int h = static_cast<int>(i % p.cache.heads);
+  i /= p.cache.heads;
+  const int first_tile = static_cast<int>(i % p.row_tiles);
+  const int64_t b = i / p.row_tiles;
+  int64_t r0, r1, len;
+  if (!sequence(p.batch, p.cache.page_tokens, b, &r0, &r1, &len)) {
+    if (threadIdx.x == 0) record_status(p.status, kStatusRange);
+    return;
+  }
+  const int64_t n = r1 - r0, tiles = (n * p.group + kRows - 1) / kRows;
+  uint32_t phase = 0;  // bit s: the parity of the warp's stage s to wait for next
+  for (int64_t rt = first_tile; rt < tiles; rt += p.row_tiles) {
+    attend<D, TERMS, NT>(p, smem, b, h, static_cast<int>(rt), piece, r0, n, len, phase);
+    fence_proxy_async_smem();  // the joined sums lie where the next bulk copies go
+    __syncthreads();
+  }
+}
+
+// Joins the pieces of one query row (a CTA each), in piece order.
+template <int D, bool F32>
+__global__ void __launch_bounds__(kWarps * 32) kv_join_kernel(const AttnParams p, int rows_per_tile) {
+  __shared__ int64_t seq[4];
+  __shared__ float so[kWarps][D];
+  __shared__ float2 sml[kWarps];
+  pdl_wait();
+  pdl_launch_dependents();
+  const int64_t row = blockIdx.x;               // token * q_heads + head
+  const int64_t t = row / p.q_heads;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) seq[0] = -1;
+  __syncthreads();
+  if (p.batch.offsets == nullptr) {
+    if (threadIdx.x == 0) seq[0] = t;
+  } else {
+    for (int64_t b = threadIdx.x; b < p.batch.B; b += blockDim.x)
+      if (p.batch.offsets[b] <= t && t < p.batch.offsets[b + 1]) seq[0] = b;
+  }
+  __syncthreads();
+  const int64_t b = seq[0];
+  if (b < 0) return;  // a row of no sequence: left as it is
+  int64_t r0, r1, len;
+  if (!sequence(p.batch, p.cache.page_tokens, b, &r0, &r1, &len)) return;
+  const int64_t n = r1 - r0;
+  const int64_t in = (t - r0) * p.group + row % p.q_heads % p.group;
+  const int64_t row0 = in / rows_per_tile * rows_per_tile;
+  const int64_t last = row0 + rows_per_tile < n * p.group ? row0 + rows_per_tile : n * p.group;
+  int64_t lo, hi;
+  visible(len, n, row0 / p.group, (last - 1) / p.group, p.window, &lo, &hi);
+  int64_t pieces = hi > lo ? (hi - lo + p.piece - 1) / p.piece : 0;
+  if (pieces > p.pieces) pieces = p.pieces;
+
+  constexpr int kPer = D / 32;
+  float top = -INFINITY, sum = 0.0f, x[kPer];
+#pragma unroll
+  for (int e = 0; e < kPer; ++e) x[e] = 0.0f;
+  for (int64_t i = warp; i < pieces; i += kWarps) {
+    const int64_t at = i * p.batch.T * p.q_heads + row;
+    const float2 ml = p.part_ml[at];
+    float v[kPer];
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) v[e] = p.part_o[at * D + lane * kPer + e];
+    if (ml.x == -INFINITY && ml.y == 0.0f) continue;  // (a NaN sum goes on)
+    const float to = fmaxf(top, ml.x);
+    const float f = top == -INFINITY ? 0.0f : ex2(top - to), a = ex2(ml.x - to);
+    sum = __fmaf_rn(sum, f, ml.y * a);
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) x[e] = __fmaf_rn(x[e], f, v[e] * a);
+    top = to;
+  }
+#pragma unroll
+  for (int e = 0; e < kPer; ++e) so[warp][lane * kPer + e] = x[e];
+  if (lane == 0) sml[warp] = make_float2(top, sum);
+  __syncthreads();
+  for (int d = threadIdx.x; d < D; d += kWarps * 32) {
+    float all = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) all = fmaxf(all, sml[w].x);
+    float y = 0.0f, z = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      const float f = sml[w].x == -INFINITY ? 0.0f : ex2(sml[w].x - all);
+      y = __fmaf_rn(f, so[w][d], y);
+      z = __fmaf_rn(f, sml[w].y, z);
+    }
+    const float out = z == 0.0f ? 0.0f : __fdiv_rn(y, z);
+    if (F32)
+      static_cast<float *>(p.o)[row * D + d] = out;
+    else
+      static_cast<__nv_bfloat16 *>(p.o)[row * D + d] = __float2bfloat16_rn(out);
+  }
+}
+
+// How a call is cut: column tiles per CTA, row tiles per sequence, pieces.
+struct AttnPlan {
+  int nt, rows;
+  int64_t row_tiles, piece, pieces;
+};
+constexpr int64_t kSms = 148;
+AttnPlan plan_of(const KvCache &cache, const KvBatch &batch, const AttnArgs &args) {
+  AttnPlan a;
+  const int terms = args.kind == kF32 ? 2 : 1;
+  const int64_t G = args.q_heads / cache.heads;
+  const int64_t need = G * (args.max_new < 1 ? 1 : args.max_new);
+  a.nt = need * terms > 8 ? 2 : 1;
+  a.rows = 8 * a.nt / terms;
+  a.row_tiles = ceil_div(need, a.rows);
+  int64_t span = batch.max_pages * cache.page_tokens;
+  if (args.window > 0 && args.window + a.rows + kChunk < span) span = args.window + a.rows + kChunk;
+  const int64_t units = batch.B * cache.heads * a.row_tiles;
+  const int64_t target = kSms * 8;
+  int64_t piece = ceil_div(ceil_div(span * units, target), 128) * 128;
+  if (piece < 128) piece = 128;
+  a.pieces = ceil_div(span, piece);
+  if (a.pieces <= 1 || units >= target) {
+    a.pieces = 1;
+    piece = (int64_t(1) << 40);
+  }
+  a.piece = piece;
+  return a;
+}
+size_t align256(size_t n) { return (n + 255) & ~size_t(255); }
+
+template <int D, int TERMS>
+cudaError_t launch(const AttnParams &p, const AttnPlan &a, const LaunchCtx &ctx) {
+  const int64_t blocks = p.batch.B * a.row_tiles * p.cache.heads * a.pieces;
+  auto kernel = a.nt == 2 ? kv_attention_kernel<D, TERMS, 2> : kv_attention_kernel<D, TERMS, 1>;
+  constexpr size_t smem = attn_smem<D>();
+  static std::atomic<uint64_t> ready[2];  // bit d: device d allows the kernel its shared memory
+  cudaError_t e = allow_smem(kernel, smem, ready[a.nt - 1], ctx);
+  if (e != cudaSuccess) return e;
+  e = launch_k(kernel, dim3(static_cast<unsigned>(blocks)), dim3(kWarps * 32), smem, ctx, p);
+  if (e != cudaSuccess || a.pieces == 1) return e;
+  return launch_k(kv_join_kernel<D, TERMS == 2>, dim3(static_cast<unsigned>(p.batch.T * p.q_heads)),
+                  dim3(kWarps * 32), 0, ctx, p, a.rows);
+}
+
+}  // namespace
+
+size_t kv_attention_workspace(const KvCache &cache, const KvBatch &batch, const AttnArgs &args) {
+  const AttnPlan a = plan_of(cache, batch, args);
+  if (a.pieces == 1) return 0;
+  const size_t rows = static_cast<size_t>(a.pieces) * batch.T * args.q_heads;
+  return align256(rows * cache.head_dim * sizeof(float)) + align256(rows * sizeof(float2));
+}
+
+bool kv_attention_fits(const KvCache &cache, const KvBatch &batch, const AttnArgs &args) {
+  const AttnPlan a = plan_of(cache, batch, args);
+  const int64_t most = (int64_t(1) << 31) - 1;
+  return a.row_tiles <= most && batch.B * a.row_tiles <= most / cache.heads &&
+         batch.B * a.row_tiles * cache.heads <= most / a.pieces &&
+         (a.pieces == 1 || batch.T <= most / args.q_heads);
+}
+
+cudaError_t launch_kv_attention(const KvCache &cache, const KvBatch &batch, const AttnArgs &args,
+                                void *workspace, const LaunchCtx &ctx) {
+  const AttnPlan a = plan_of(cache, batch, args);
+  AttnParams p = {};
+  p.cache = cache;
+  p.batch = batch;
+  p.q = args.Q;
+  p.o = args.O;
+  p.q_heads = args.q_heads;
+  p.group = args.q_heads / cache.heads;
+  p.scale_log2 = args.scale * kLog2e;
+  p.window = args.window;
+  p.row_tiles = static_cast<int>(a.row_tiles);
+  p.pieces = static_cast<int>(a.pieces);
+  p.piece = a.piece;
+  p.status = ctx.status;
+  if (a.pieces > 1) {
+    const size_t rows = static_cast<size_t>(a.pieces) * batch.T * args.q_heads;
+    p.part_o = static_cast<float *>(workspace);
+    p.part_ml = reinterpret_cast<float2 *>(static_cast<uint8_t *>(workspace) +
+                                           align256(rows * cache.head_dim * sizeof(float)));
+  }
+  if (args.kind == kF32)
+    return cache.head_dim == 128 ? launch<128, 2>(p, a, ctx) : launch<64, 2>(p, a, ctx);
+  return cache.head_dim == 128 ? launch<128, 1>(p, a, ctx) : launch<64, 1>(p, a, ctx);
+}
+
+}  // namespace bitnet
