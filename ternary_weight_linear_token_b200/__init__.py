@@ -488,32 +488,34 @@ def bitnet_decode_chain(steps, x0: torch.Tensor, workspace: torch.Tensor,
 
 # ---------------------------------------------------------------- decode step: cache, attention, head
 # These entry points run on the device of their tensors, whichever is current,
-# and take `stream` (default: that device's current stream) for the tensors
-# that they allocate as well.
-def _on(stream, *tensors):
-    """Checks that the tensors share a CUDA device; (context to run in or
-    None, raw stream) for a call on them."""
-    dev = tensors[0].device
-    for t in tensors:
-        if t.device != dev:
-            if not t.is_cuda:
-                raise ValueError("tensors must be CUDA tensors (there is no CPU fallback)")
-            raise ValueError(f"tensors are on {dev} and on {t.device}")
-    if not tensors[0].is_cuda:
-        raise ValueError("tensors must be CUDA tensors (there is no CPU fallback)")
+# and allocate on the stream that they run on.  A decode step calls them for
+# every token, so each checks its tensors by the cheapest calls there are and
+# takes the raw stream of the current device; another device or a given
+# stream goes through _elsewhere.
+_raw_stream = torch._C._cuda_getCurrentRawStream
+_current_device = torch._C._cuda_getDevice
+_FLOAT = {torch.float32: F32, torch.bfloat16: BF16}
+
+
+def _elsewhere(device: int, stream, call, *args, **kwargs):
+    """call(*args, **kwargs) with the tensors' device, and `stream`, current."""
     if stream is None:
-        raw = torch._C._cuda_getCurrentRawStream(dev.index)
-        return (None if dev.index == torch._C._cuda_getDevice() else torch.cuda.device(dev)), raw
-    if stream.device != dev:
-        raise ValueError(f"stream is on {stream.device}, the tensors on {dev}")
-    return torch.cuda.stream(stream), stream.cuda_stream
+        with torch.cuda.device(device):
+            return call(*args, **kwargs)
+    if stream.device.index != device:
+        raise ValueError(f"stream is on {stream.device}, the tensors on cuda:{device}")
+    with torch.cuda.stream(stream):
+        return call(*args, **kwargs)
 
 
-def _within(context, call):
-    if context is None:
-        return call()
-    with context:
-        return call()
+def _same_device(device: int, **tensors):
+    """Raises the fitting error: `device` (of the first tensor) is no CUDA
+    device, or one of the tensors is on another one."""
+    if device < 0:
+        raise ValueError("tensors must be CUDA tensors (there is no CPU fallback)")
+    for name, t in tensors.items():
+        if t is not None and t.get_device() != device:
+            raise ValueError(f"{name} must be on cuda:{device}, it is on {t.device}")
 
 
 def _is(t: torch.Tensor, name: str, *dtypes):
@@ -522,7 +524,8 @@ def _is(t: torch.Tensor, name: str, *dtypes):
 
 
 def _dense(t: torch.Tensor, name: str, *dtypes):
-    _is(t, name, *dtypes)
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name} must have dtype in {dtypes}, got {t.dtype}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
 
@@ -559,12 +562,12 @@ class KVCache:
             raise ValueError("k_codes and v_codes must be [num_pages, heads, page_tokens, head_dim]")
         if k_scales.shape != k_codes.shape[:2] or v_scales.shape != k_codes.shape[:2]:
             raise ValueError("k_scales and v_scales must be [num_pages, heads]")
-        if len({t.device for t in (k_codes, v_codes, k_scales, v_scales)}) != 1:
-            raise ValueError("a cache lies on one device")
+        self.device = k_codes.get_device()
+        _same_device(self.device, v_codes=v_codes, k_scales=k_scales, v_scales=v_scales)
         self.k_codes, self.v_codes, self.k_scales, self.v_scales = k_codes, v_codes, k_scales, v_scales
         self.num_pages, self.heads, self.page_tokens, self.head_dim = k_codes.shape
         self._struct = KVCacheStruct(k_codes.data_ptr(), v_codes.data_ptr(), k_scales.data_ptr(),
-                                     v_scales.data_ptr(), *(k_codes.shape[i] for i in (0, 1, 2, 3)))
+                                     v_scales.data_ptr(), *k_codes.shape)
         self._ref = C.addressof(self._struct)
 
 
@@ -573,16 +576,16 @@ def _batch(pages, lens, offsets, T, max_new):
     _dense(pages, "pages", torch.int32)
     _dense(lens, "lens", torch.int32)
     B = lens.numel()
-    if pages.dim() != 2 or pages.shape[0] != B or lens.dim() != 1:
+    if pages.dim() != 2 or pages.size(0) != B or lens.dim() != 1:
         raise ValueError("pages must be [B, max_pages] and lens [B]")
     if offsets is None:
         if T != B:
             raise ValueError(f"{T} rows for {B} sequences: without offsets every sequence has one")
-        return B, pages.shape[1], 1
+        return B, pages.size(1), 1
     _dense(offsets, "offsets", torch.int32)
     if offsets.numel() != B + 1:
         raise ValueError(f"offsets has {offsets.numel()} elements, expected B + 1 = {B + 1}")
-    return B, pages.shape[1], T if max_new is None else int(max_new)
+    return B, pages.size(1), T if max_new is None else int(max_new)
 
 
 def bitnet_kv_append(cache: KVCache, K: torch.Tensor, V: torch.Tensor, pages: torch.Tensor,
@@ -594,21 +597,30 @@ def bitnet_kv_append(cache: KVCache, K: torch.Tensor, V: torch.Tensor, pages: to
     [B + 1] int32 say where: rows offsets[b] .. offsets[b + 1] - 1 are the
     last tokens of sequence b; without offsets each sequence has one row.
     ``max_new``: the most rows of a sequence (default: T)."""
-    T = K.shape[0]
-    _is(K, "K", torch.float32, torch.bfloat16)
-    _is(V, "V", K.dtype)
+    kind = _FLOAT.get(K.dtype)
+    if kind is None or V.dtype != K.dtype:
+        raise TypeError(f"K and V must both be fp32 or bf16, got {K.dtype} and {V.dtype}")
     H, D = cache.heads, cache.head_dim
-    if K.shape != (T, H, D) or V.shape != (T, H, D):
+    shape = K.shape
+    if len(shape) != 3 or shape[1] != H or shape[2] != D or V.shape != shape:
         raise ValueError(f"K and V must be [T, {H}, {D}]")
+    T = shape[0]
     ks, vs = K.stride(), V.stride()
     if T > 0 and not (ks[2] == vs[2] == 1 and (H == 1 or ks[1] == vs[1] == D)):
         raise ValueError("the heads of a token must lie one after the other in K and V")
     B, W, most = _batch(pages, lens, offsets, T, max_new)
-    ctx, raw = _on(stream, cache.k_codes, K, V, pages, lens, *(() if offsets is None else (offsets,)))
-    st = _within(ctx, lambda: lib.bitnet_kv_append(
-        cache._ref, K.data_ptr(), ks[0], V.data_ptr(), vs[0], _DTYPE[K.dtype], T, pages.data_ptr(), W,
-        lens.data_ptr(), None if offsets is None else offsets.data_ptr(), B, most, raw))
-    _check(st, "bitnet_kv_append")
+    d = K.get_device()
+    if d < 0 or not (d == cache.device == V.get_device() == pages.get_device() == lens.get_device()):
+        _same_device(d, cache=cache.k_codes, V=V, pages=pages, lens=lens)
+    if offsets is not None and offsets.get_device() != d:
+        _same_device(d, offsets=offsets)
+    if stream is not None or d != _current_device():
+        return _elsewhere(d, stream, bitnet_kv_append, cache, K, V, pages, lens, offsets, max_new)
+    st = lib.bitnet_kv_append(
+        cache._ref, K.data_ptr(), ks[0], V.data_ptr(), vs[0], kind, T, pages.data_ptr(), W, lens.data_ptr(),
+        None if offsets is None else offsets.data_ptr(), B, most, _raw_stream(d))
+    if st:
+        _check(st, "bitnet_kv_append")
 
 
 @functools.lru_cache(maxsize=1024)
@@ -619,7 +631,7 @@ def _kv_workspace(num_pages, heads, page_tokens, head_dim, dtype, T, q_heads, B,
 
 def bitnet_kv_attention_workspace_size(cache: KVCache, dtype: torch.dtype, T: int, q_heads: int, B: int,
                                        max_pages: int, max_new: int = 1, window: int = 0) -> int:
-    return _kv_workspace(cache.num_pages, cache.heads, cache.page_tokens, cache.head_dim, _DTYPE[dtype],
+    return _kv_workspace(cache.num_pages, cache.heads, cache.page_tokens, cache.head_dim, _FLOAT[dtype],
                          int(T), int(q_heads), int(B), int(max_pages), int(max_new), int(window))
 
 
@@ -635,34 +647,48 @@ def bitnet_kv_attention(cache: KVCache, Q: torch.Tensor, pages: torch.Tensor, le
     ``workspace`` (``bitnet_kv_attention_workspace_size`` bytes) one is
     allocated.  Rows of no sequence are left as O has them (a new O: as its
     memory was)."""
-    _dense(Q, "Q", torch.float32, torch.bfloat16)
-    if Q.dim() != 3 or Q.shape[2] != cache.head_dim:
-        raise ValueError(f"Q must be [T, q_heads, {cache.head_dim}]")
-    T, q_heads, D = Q.shape
+    kind = _FLOAT.get(Q.dtype)
+    if kind is None:
+        raise TypeError(f"Q must be fp32 or bf16, got {Q.dtype}")
+    if not Q.is_contiguous():
+        raise ValueError("Q must be contiguous")
+    D = cache.head_dim
+    if Q.dim() != 3 or Q.size(2) != D:
+        raise ValueError(f"Q must be [T, q_heads, {D}]")
+    T, q_heads = Q.size(0), Q.size(1)
     B, W, most = _batch(pages, lens, offsets, T, max_new)
-    ctx, raw = _on(stream, cache.k_codes, Q, pages, lens, *(() if offsets is None else (offsets,)),
-                   *(() if O is None else (O,)), *(() if workspace is None else (workspace,)))
-    if O is not None:
+    d = Q.get_device()
+    if d < 0 or not (d == cache.device == pages.get_device() == lens.get_device()):
+        _same_device(d, cache=cache.k_codes, pages=pages, lens=lens)
+    if offsets is not None and offsets.get_device() != d:
+        _same_device(d, offsets=offsets)
+    if stream is not None or d != _current_device():
+        return _elsewhere(d, stream, bitnet_kv_attention, cache, Q, pages, lens, offsets, max_new, scale,
+                          window, O, workspace)
+    if O is None:
+        O = torch.empty_like(Q)
+    else:
         _dense(O, "O", Q.dtype)
+        _same_device(d, O=O)
         if O.shape != Q.shape:
             raise ValueError("O must have the shape of Q")
-    need = _kv_workspace(cache.num_pages, cache.heads, cache.page_tokens, D, _DTYPE[Q.dtype], T, q_heads, B,
-                         W, most, int(window))
-
-    def call():
-        out, ws = O, workspace
-        if out is None:
-            out = torch.empty_like(Q)
-        if ws is None and need > 0:
-            ws = torch.empty(need, dtype=torch.uint8, device=Q.device)
-        return lib.bitnet_kv_attention(
-            cache._ref, Q.data_ptr(), out.data_ptr(), _DTYPE[Q.dtype], T, q_heads, pages.data_ptr(), W,
-            lens.data_ptr(), None if offsets is None else offsets.data_ptr(), B, most,
-            D ** -0.5 if scale is None else scale, window, None if ws is None else ws.data_ptr(),
-            0 if ws is None else ws.numel() * ws.element_size(), raw), out
-    st, out = _within(ctx, call)
-    _check(st, "bitnet_kv_attention")
-    return out
+    ws, size = 0, 0
+    if workspace is None:
+        size = _kv_workspace(cache.num_pages, cache.heads, cache.page_tokens, D, kind, T, q_heads, B, W, most,
+                             window)
+        if size > 0:
+            workspace = torch.empty(size, dtype=torch.uint8, device=Q.device)
+            ws = workspace.data_ptr()
+    else:
+        _same_device(d, workspace=workspace)
+        ws, size = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    st = lib.bitnet_kv_attention(
+        cache._ref, Q.data_ptr(), O.data_ptr(), kind, T, q_heads, pages.data_ptr(), W, lens.data_ptr(),
+        None if offsets is None else offsets.data_ptr(), B, most, D ** -0.5 if scale is None else scale, window,
+        ws, size, _raw_stream(d))
+    if st:
+        _check(st, "bitnet_kv_attention")
+    return O
 
 
 def bitnet_quantize_weights_w4(W: torch.Tensor, group: int = 128, packed: torch.Tensor | None = None,
@@ -673,24 +699,31 @@ def bitnet_quantize_weights_w4(W: torch.Tensor, group: int = 128, packed: torch.
     if group not in (32, 64, 128):
         raise ValueError(f"group must be 32, 64 or 128, got {group}")
     N, K = W.shape
-    ctx, raw = _on(stream, W, *(t for t in (packed, scales) if t is not None))
-
-    def call():
-        p = torch.empty((N, K // 2), dtype=torch.uint8, device=W.device) if packed is None else packed
-        s = torch.empty((N, K // group), dtype=torch.bfloat16, device=W.device) if scales is None else scales
-        _dense(p, "packed", torch.uint8)
-        _dense(s, "scales", torch.bfloat16)
-        if p.shape != (N, K // 2) or s.shape != (N, K // group):
-            raise ValueError("packed must be [N, K/2] and scales [N, K/group]")
-        return lib.bitnet_quantize_weights_w4(W.data_ptr(), _DTYPE[W.dtype], N, K, group, p.data_ptr(),
-                                              s.data_ptr(), raw), p, s
-    st, p, s = _within(ctx, call)
+    d = W.get_device()
+    _same_device(d, packed=packed, scales=scales)
+    if stream is not None or d != _current_device():
+        return _elsewhere(d, stream, bitnet_quantize_weights_w4, W, group, packed, scales)
+    if packed is None:
+        packed = torch.empty((N, K // 2), dtype=torch.uint8, device=W.device)
+    if scales is None:
+        scales = torch.empty((N, K // group), dtype=torch.bfloat16, device=W.device)
+    _dense(packed, "packed", torch.uint8)
+    _dense(scales, "scales", torch.bfloat16)
+    if packed.shape != (N, K // 2) or scales.shape != (N, K // group):
+        raise ValueError("packed must be [N, K/2] and scales [N, K/group]")
+    st = lib.bitnet_quantize_weights_w4(W.data_ptr(), _FLOAT[W.dtype], N, K, group, packed.data_ptr(),
+                                        scales.data_ptr(), _raw_stream(d))
     _check(st, "bitnet_quantize_weights_w4")
-    return p, s
+    return packed, scales
 
 
 def bitnet_w4a16_matmul_workspace_size(M: int, N: int, K: int, x_dtype: torch.dtype) -> int:
-    return lib.bitnet_w4a16_matmul_workspace_size(M, N, K, _DTYPE[x_dtype])
+    return _w4_workspace(int(M), int(N), int(K), _FLOAT[x_dtype])
+
+
+@functools.lru_cache(maxsize=1024)
+def _w4_workspace(M, N, K, kind):
+    return lib.bitnet_w4a16_matmul_workspace_size(M, N, K, kind)
 
 
 def bitnet_w4a16_matmul(X: torch.Tensor, packed: torch.Tensor, scales: torch.Tensor,
@@ -700,39 +733,50 @@ def bitnet_w4a16_matmul(X: torch.Tensor, packed: torch.Tensor, scales: torch.Ten
     """Y [M, N] = X [M, K] (fp32/bf16) times the transpose of the 4-bit
     weights of ``bitnet_quantize_weights_w4``; Y fp32/bf16.  Made for few
     tokens (a decode step); more run in blocks."""
-    _dense(X, "X", torch.float32, torch.bfloat16)
-    _dense(packed, "packed", torch.uint8)
-    _dense(scales, "scales", torch.bfloat16)
-    M, K = X.shape
-    N = packed.shape[0]
-    if packed.shape[1] * 2 != K:
-        raise ValueError(f"packed has {packed.shape[1]} bytes per row, expected K/2 = {K // 2}")
-    groups = scales.shape[1] if scales.dim() == 2 else 0
-    if groups == 0 or scales.shape[0] != N or K % groups != 0:
+    kind = _FLOAT.get(X.dtype)
+    if kind is None:
+        raise TypeError(f"X must be fp32 or bf16, got {X.dtype}")
+    if packed.dtype is not torch.uint8 or scales.dtype is not torch.bfloat16:
+        raise TypeError(f"packed must be uint8 and scales bf16, got {packed.dtype} and {scales.dtype}")
+    if not (X.is_contiguous() and packed.is_contiguous() and scales.is_contiguous()):
+        raise ValueError("X, packed and scales must be contiguous")
+    if not X.dim() == packed.dim() == scales.dim() == 2:
+        raise ValueError("X must be [M, K], packed [N, K/2] and scales [N, K/group]")
+    M, K, N, groups = X.size(0), X.size(1), packed.size(0), scales.size(1)
+    if packed.size(1) * 2 != K:
+        raise ValueError(f"packed has {packed.size(1)} bytes per row, expected K/2 = {K // 2}")
+    if groups == 0 or scales.size(0) != N or K % groups != 0:
         raise ValueError("scales must be [N, K/group]")
-    ctx, raw = _on(stream, X, packed, scales, *(t for t in (Y, workspace) if t is not None))
-    if Y is not None:
-        _dense(Y, "Y", torch.float32, torch.bfloat16)
-        if Y.shape != (M, N):
-            raise ValueError(f"Y must be [{M}, {N}]")
-
-    def call():
-        out, ws = Y, workspace
-        if out is None:
-            out = torch.empty((M, N), dtype=out_dtype, device=X.device)
-            _is(out, "out_dtype", torch.float32, torch.bfloat16)
-        if ws is None:
-            need = lib.bitnet_w4a16_matmul_workspace_size(M, N, K, _DTYPE[X.dtype])
-            if need > 0:
-                ws = torch.empty(need, dtype=torch.uint8, device=X.device)
-        return lib.bitnet_w4a16_matmul(
-            X.data_ptr(), _DTYPE[X.dtype], packed.data_ptr(), scales.data_ptr(), M, N, K, K // groups,
-            out.data_ptr(), _DTYPE[out.dtype], None if ws is None else ws.data_ptr(),
-            0 if ws is None else ws.numel() * ws.element_size(),
-            FLAG_WEIGHTS_STATIC if weights_static else 0, raw), out
-    st, out = _within(ctx, call)
-    _check(st, "bitnet_w4a16_matmul")
-    return out
+    d = X.get_device()
+    if d < 0 or not (d == packed.get_device() == scales.get_device()):
+        _same_device(d, packed=packed, scales=scales)
+    if stream is not None or d != _current_device():
+        return _elsewhere(d, stream, bitnet_w4a16_matmul, X, packed, scales, out_dtype, Y, workspace,
+                          weights_static)
+    if Y is None:
+        Y = X.new_empty((M, N)) if out_dtype is X.dtype else torch.empty((M, N), dtype=out_dtype, device=X.device)
+    else:
+        _same_device(d, Y=Y)
+        if Y.shape != (M, N) or not Y.is_contiguous():
+            raise ValueError(f"Y must be [{M}, {N}] and contiguous")
+    y_kind = _FLOAT.get(Y.dtype)
+    if y_kind is None:
+        raise TypeError(f"Y must be fp32 or bf16, got {Y.dtype}")
+    ws, size = 0, 0
+    if workspace is not None:
+        _same_device(d, workspace=workspace)
+        ws, size = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    else:
+        size = _w4_workspace(M, N, K, kind)
+        if size > 0:
+            workspace = torch.empty(size, dtype=torch.uint8, device=X.device)
+            ws = workspace.data_ptr()
+    st = lib.bitnet_w4a16_matmul(X.data_ptr(), kind, packed.data_ptr(), scales.data_ptr(), M, N, K, K // groups,
+                                 Y.data_ptr(), y_kind, ws, size, FLAG_WEIGHTS_STATIC if weights_static else 0,
+                                 _raw_stream(d))
+    if st:
+        _check(st, "bitnet_w4a16_matmul")
+    return Y
 
 
 def bitnet_token_logprobs(logits: torch.Tensor, tokens: torch.Tensor, top: int = 0, stream=None):
@@ -741,25 +785,33 @@ def bitnet_token_logprobs(logits: torch.Tensor, tokens: torch.Tensor, top: int =
     top_logprobs [M, top]), all but the ids fp32.  tokens [M] int64; a
     negative one asks for no log probability (0).  ``top`` <= 32 alternatives
     come most probable first, equal ones by the lower id."""
-    _is(logits, "logits", torch.float32, torch.bfloat16)
-    _dense(tokens, "tokens", torch.int64)
-    M, V = logits.shape
-    if tokens.shape != (M,):
-        raise ValueError(f"tokens must be [{M}]")
+    kind = _FLOAT.get(logits.dtype)
+    if kind is None:
+        raise TypeError(f"logits must be fp32 or bf16, got {logits.dtype}")
+    if tokens.dtype is not torch.int64:
+        raise TypeError(f"tokens must be int64, got {tokens.dtype}")
+    if logits.dim() != 2:
+        raise ValueError("logits must be [M, V]")
+    M, V = logits.size(0), logits.size(1)
+    if tokens.dim() != 1 or tokens.size(0) != M or not tokens.is_contiguous():
+        raise ValueError(f"tokens must be [{M}] and contiguous")
     if V > 1 and logits.stride(1) != 1:
         raise ValueError("the values of a row of logits must be contiguous")
-    ctx, raw = _on(stream, logits, tokens)
-
-    def call():
-        dev = logits.device
-        lp = torch.empty((2, M), dtype=torch.float32, device=dev)
-        ids = torch.empty((M, max(top, 0)), dtype=torch.int64, device=dev)
-        tl = torch.empty((M, max(top, 0)), dtype=torch.float32, device=dev)
-        at = lp.data_ptr()
-        return lib.bitnet_token_logprobs(
-            logits.data_ptr(), _DTYPE[logits.dtype], M, V, logits.stride(0), tokens.data_ptr(), top, at,
-            at + 4 * M, ids.data_ptr() if top > 0 else None, tl.data_ptr() if top > 0 else None,
-            raw), (lp[0], lp[1], ids, tl)
-    st, out = _within(ctx, call)
-    _check(st, "bitnet_token_logprobs")
-    return out
+    if top < 0:
+        raise ValueError(f"top must not be negative, got {top}")
+    d = logits.get_device()
+    if d < 0 or tokens.get_device() != d:
+        _same_device(d, tokens=tokens)
+    if stream is not None or d != _current_device():
+        return _elsewhere(d, stream, bitnet_token_logprobs, logits, tokens, top)
+    dev = logits.device
+    lp = torch.empty(M, dtype=torch.float32, device=dev)
+    h = torch.empty_like(lp)
+    ids = tokens.new_empty((M, top))
+    tl = lp.new_empty((M, top))
+    st = lib.bitnet_token_logprobs(logits.data_ptr(), kind, M, V, logits.stride(0), tokens.data_ptr(), top,
+                                   lp.data_ptr(), h.data_ptr(), ids.data_ptr() if top else None,
+                                   tl.data_ptr() if top else None, _raw_stream(d))
+    if st:
+        _check(st, "bitnet_token_logprobs")
+    return lp, h, ids, tl

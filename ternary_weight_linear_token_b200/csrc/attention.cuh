@@ -1,0 +1,51 @@
+// attention.cuh -- what the attention kernels over the 8-bit cache share.
+#pragma once
+
+#include <cuda_fp16.h>
+
+#include "common.cuh"
+#include "internal.h"
+
+namespace bitnet {
+
+constexpr int kStatusRange = 6;  // == BITNET_ERR_RANGE
+constexpr float kLog2e = 1.4426950408889634f;
+// Weights are 2^(score - m + kRaise); m follows the scores once they pass it
+// by kLazy (both log2): weights stay below 2^15, and fp16 keeps them to 2^-12
+// or to 2^-32 of the largest.
+constexpr float kLazy = 8.0f;
+constexpr float kRaise = 7.0f;
+
+// The rows of sequence b and its length; false for numbers that do not
+// describe one.
+__device__ __forceinline__ bool kv_sequence(const KvBatch &batch, int P, int64_t b, int64_t *r0,
+                                         int64_t *r1, int64_t *len) {
+  *len = batch.lens[b];
+  *r0 = b;
+  *r1 = b + 1;
+  if (batch.offsets != nullptr) {
+    *r0 = batch.offsets[b];
+    *r1 = batch.offsets[b + 1];
+  }
+  return *r0 >= 0 && *r1 <= batch.T && *r0 <= *r1 && *len >= 0 && *len <= batch.max_pages * P;
+}
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ uint32_t half2_bits(__half2 h) {
+  return *reinterpret_cast<uint32_t *>(&h);
+}
+// Two codes + 128, one in the low byte of each half, to two halves.
+__device__ __forceinline__ uint32_t from_biased(uint32_t x) {
+  const uint32_t bias = 0x64806480u;  // 1152, twice
+  return half2_bits(__hsub2(*reinterpret_cast<__half2 *>(&x), *reinterpret_cast<const __half2 *>(&bias)));
+}
+// Bytes 0, 1 (2, 3) of w (codes + 128) as two halves.
+__device__ __forceinline__ uint32_t codes01(uint32_t w) { return from_biased(__byte_perm(w, 0x64646464u, 0x4140)); }
+__device__ __forceinline__ uint32_t codes23(uint32_t w) { return from_biased(__byte_perm(w, 0x64646464u, 0x4342)); }
+
+}  // namespace bitnet

@@ -190,6 +190,11 @@ bool kv_attention_fits(const KvCache &cache, const KvBatch &batch, const AttnArg
 cudaError_t launch_kv_attention(const KvCache &cache, const KvBatch &batch, const AttnArgs &args,
                                 void *workspace, const LaunchCtx &ctx);
 
+// kv_attention_prompt.cu: many bf16 queries per sequence.
+bool kv_attention_prompt_fits(const KvCache &cache, const KvBatch &batch, const AttnArgs &args);
+cudaError_t launch_kv_attention_prompt(const KvCache &cache, const KvBatch &batch, const AttnArgs &args,
+                                       const LaunchCtx &ctx);
+
 // gemv_w4.cu: 4-bit weights [N][K / 2] with bf16 scales [N][K / group].
 cudaError_t launch_quantize_weights_w4(const void *W, int w_kind, int64_t N, int64_t K, int group,
                                        uint8_t *packed, uint16_t *scales, const LaunchCtx &ctx);

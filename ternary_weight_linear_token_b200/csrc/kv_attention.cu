@@ -30,22 +30,17 @@
 // of a chunk are contiguous in a page), page numbers and scales fetched
 // ahead; they join their sums in shared memory.  Few rows over a long cache
 // are cut into pieces, which a second kernel joins in piece order.
-#include <cuda_fp16.h>
-
 #include <atomic>
 
+#include "attention.cuh"
 #include "common.cuh"
 #include "internal.h"
 
 namespace bitnet {
 namespace {
 
-constexpr int kStatusRange = 6;  // == BITNET_ERR_RANGE
 constexpr int kWarps = 4;
 constexpr int kChunk = 32;       // tokens per ring stage
-constexpr float kLazy = 8.0f;    // the maximum follows the scores once they pass it by this (log2)
-constexpr float kRaise = 7.0f;
-constexpr float kLog2e = 1.4426950408889634f;
 
 struct AttnParams {
   KvCache cache;
@@ -76,20 +71,6 @@ template <int D> constexpr size_t attn_smem() {
          (Ring<D>::kStageBytes + sizeof(ChunkScales) + sizeof(uint64_t));
 }
 
-// The rows of sequence b and its length; false (and `bad` set) for numbers
-// that do not describe one.
-__device__ __forceinline__ bool sequence(const KvBatch &batch, int P, int64_t b, int64_t *r0,
-                                         int64_t *r1, int64_t *len) {
-  *len = batch.lens[b];
-  *r0 = b;
-  *r1 = b + 1;
-  if (batch.offsets != nullptr) {
-    *r0 = batch.offsets[b];
-    *r1 = batch.offsets[b + 1];
-  }
-  return *r0 >= 0 && *r1 <= batch.T && *r0 <= *r1 && *len >= 0 && *len <= batch.max_pages * P;
-}
-
 // Positions that some of the queries i0..i1 of a sequence sees: [lo, hi),
 // lo rounded down to a chunk.
 __device__ __forceinline__ void visible(int64_t len, int64_t n, int64_t i0, int64_t i1,
@@ -97,12 +78,6 @@ __device__ __forceinline__ void visible(int64_t len, int64_t n, int64_t i0, int6
   *hi = len - n + i1 + 1;
   const int64_t first = window > 0 ? len - n + i0 - window + 1 : 0;
   *lo = (first > 0 ? first : 0) / kChunk * kChunk;
-}
-
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
 }
 
 __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
@@ -120,18 +95,6 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
   return y;
 }
-
-__device__ __forceinline__ uint32_t half2_bits(__half2 h) {
-  return *reinterpret_cast<uint32_t *>(&h);
-}
-// Two codes + 128, one in the low byte of each half, to two halves.
-__device__ __forceinline__ uint32_t from_biased(uint32_t x) {
-  const uint32_t bias = 0x64806480u;  // 1152, twice
-  return half2_bits(__hsub2(*reinterpret_cast<__half2 *>(&x), *reinterpret_cast<const __half2 *>(&bias)));
-}
-// Bytes 0, 1 (2, 3) of w (codes + 128) as two halves.
-__device__ __forceinline__ uint32_t codes01(uint32_t w) { return from_biased(__byte_perm(w, 0x64646464u, 0x4140)); }
-__device__ __forceinline__ uint32_t codes23(uint32_t w) { return from_biased(__byte_perm(w, 0x64646464u, 0x4342)); }
 
 template <typename T> __device__ __forceinline__ T lds(const void *p) { return *static_cast<const T *>(p); }
 
@@ -547,7 +510,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) kv_attention_kernel(const Attn
   const int first_tile = static_cast<int>(i % p.row_tiles);
   const int64_t b = i / p.row_tiles;
   int64_t r0, r1, len;
-  if (!sequence(p.batch, p.cache.page_tokens, b, &r0, &r1, &len)) {
+  if (!kv_sequence(p.batch, p.cache.page_tokens, b, &r0, &r1, &len)) {
     if (threadIdx.x == 0) record_status(p.status, kStatusRange);
     return;
   }
@@ -583,7 +546,7 @@ __global__ void __launch_bounds__(kWarps * 32) kv_join_kernel(const AttnParams p
   const int64_t b = seq[0];
   if (b < 0) return;  // a row of no sequence: left as it is
   int64_t r0, r1, len;
-  if (!sequence(p.batch, p.cache.page_tokens, b, &r0, &r1, &len)) return;
+  if (!kv_sequence(p.batch, p.cache.page_tokens, b, &r0, &r1, &len)) return;
   const int64_t n = r1 - r0;
   const int64_t in = (t - r0) * p.group + row % p.q_heads % p.group;
   const int64_t row0 = in / rows_per_tile * rows_per_tile;
@@ -678,9 +641,15 @@ cudaError_t launch(const AttnParams &p, const AttnPlan &a, const LaunchCtx &ctx)
                   dim3(kWarps * 32), 0, ctx, p, a.rows);
 }
 
+// Prompts of bf16 queries go to the tcgen05 kernel.
+bool use_prompt(const KvCache &cache, const AttnArgs &args) {
+  return args.kind == kBF16 && args.max_new * (args.q_heads / cache.heads) >= 128;
+}
+
 }  // namespace
 
 size_t kv_attention_workspace(const KvCache &cache, const KvBatch &batch, const AttnArgs &args) {
+  if (use_prompt(cache, args)) return 0;
   const AttnPlan a = plan_of(cache, batch, args);
   if (a.pieces == 1) return 0;
   const size_t rows = static_cast<size_t>(a.pieces) * batch.T * args.q_heads;
@@ -688,6 +657,7 @@ size_t kv_attention_workspace(const KvCache &cache, const KvBatch &batch, const 
 }
 
 bool kv_attention_fits(const KvCache &cache, const KvBatch &batch, const AttnArgs &args) {
+  if (use_prompt(cache, args)) return kv_attention_prompt_fits(cache, batch, args);
   const AttnPlan a = plan_of(cache, batch, args);
   const int64_t most = (int64_t(1) << 31) - 1;
   return a.row_tiles <= most && batch.B * a.row_tiles <= most / cache.heads &&
@@ -697,6 +667,7 @@ bool kv_attention_fits(const KvCache &cache, const KvBatch &batch, const AttnArg
 
 cudaError_t launch_kv_attention(const KvCache &cache, const KvBatch &batch, const AttnArgs &args,
                                 void *workspace, const LaunchCtx &ctx) {
+  if (use_prompt(cache, args)) return launch_kv_attention_prompt(cache, batch, args, ctx);
   const AttnPlan a = plan_of(cache, batch, args);
   AttnParams p = {};
   p.cache = cache;
