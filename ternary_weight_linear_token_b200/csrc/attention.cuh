@@ -48,4 +48,19 @@ __device__ __forceinline__ uint32_t from_biased(uint32_t x) {
 __device__ __forceinline__ uint32_t codes01(uint32_t w) { return from_biased(__byte_perm(w, 0x64646464u, 0x4140)); }
 __device__ __forceinline__ uint32_t codes23(uint32_t w) { return from_biased(__byte_perm(w, 0x64646464u, 0x4342)); }
 
+// mbar_wait in few instructions (its retries unrolled would fill the
+// instruction cache of kernels that wait in many places).
+__device__ __forceinline__ bool wait_for(uint64_t *bar, uint32_t parity, int *status) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const long long t0 = clock64();
+#pragma unroll 1
+  while (!mbar_try_wait(bar, parity)) {
+    if (clock64() - t0 > kWaitLimitCycles) {
+      record_status(status, kStatusTimeout);
+      return false;
+    }
+  }
+  return true;
+}
+
 }  // namespace bitnet
