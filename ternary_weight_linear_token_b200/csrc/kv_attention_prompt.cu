@@ -276,14 +276,14 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_prompt_kernel(const 
       // q to shared memory, its largest value brought to [2^14, 2^15)
       float fac;
       {
-        auto load_q = [&](int c) {
-          return have ? __ldg(reinterpret_cast<const uint4 *>(p.q + at) + c) : make_uint4(0, 0, 0, 0);
-        };
+        uint4 v[D / 8];
+#pragma unroll
+        for (int c = 0; c < D / 8; ++c)
+          v[c] = have ? __ldg(reinterpret_cast<const uint4 *>(p.q + at) + c) : make_uint4(0, 0, 0, 0);
         uint32_t peak = 0;
-#pragma unroll 4
+#pragma unroll
         for (int c = 0; c < D / 8; ++c) {
-          const uint4 v = load_q(c);
-          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+          const uint32_t w[4] = {v[c].x, v[c].y, v[c].z, v[c].w};
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const uint32_t a = (w[e] << 16) & 0x7FFFFFFFu, c2 = w[e] & 0x7FFF0000u;
@@ -296,10 +296,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_prompt_kernel(const 
         const float up = __uint_as_float((static_cast<uint32_t>(127 + k) << 23) | (p.negate ? 0x80000000u : 0u));
         fac = __fmul_rn(p.scale_log2, __uint_as_float(static_cast<uint32_t>(127 - k) << 23));
         uint8_t *tile = smem + S::kQ + t * S::kOperand;
-#pragma unroll 4
+#pragma unroll
         for (int c = 0; c < D / 8; ++c) {
-          const uint4 v = load_q(c);
-          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+          const uint32_t w[4] = {v[c].x, v[c].y, v[c].z, v[c].w};
           uint32_t o[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
@@ -316,7 +315,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_prompt_kernel(const 
       const uint32_t ts = tmem + lanes + t * kTile, to = tmem + lanes + 2 * kTile + t * D;
       const int pos = static_cast<int>(len - n + query);
       const int first = p.window > 0 && pos - p.window + 1 > 0 ? static_cast<int>(pos - p.window + 1) : 0;
-      float m = -INFINITY, l = 0.0f;
+      float m = -INFINITY, l = 0.0f;  // m is whole
       for (int j = 0; j < mine && ok; ++j) {
         const int slot = static_cast<int>((done + j) % kSlots);
         const uint32_t tj = before + j;
@@ -330,28 +329,79 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_prompt_kernel(const 
         bool part = c_hi < kTile || c_lo > 0;
 #pragma unroll
         for (int s = 0; s < kSegs; ++s) part |= sc.ks[s] < 0.0f;
-        // 32 columns at a time, the next ones on their way: weights by the
-        // maximum in use, written over scores that have been read.  Only where
-        // a score passes the maximum by 2^kLazy (or is the row's first) does
-        // it follow, with the row's sum, O and the block's earlier weights.
-        // A block that every row of the warp sees whole takes the form without
-        // comparisons.
+        // Twice over the scores, 32 columns at a time with the next ones on
+        // their way: the row's maximum; then weights, written over scores that
+        // have been read, and their sum.  A block that every row of the warp
+        // sees whole takes the form without comparisons.
         auto weights = [&](auto masked_form) -> bool {
           constexpr bool kMasked = decltype(masked_form)::value;
           uint32_t buf[2][32];
           tmem_ld32(ts, buf[0]);
+          float top = -INFINITY;  // of score + log2 vs
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            uint32_t(&v)[32] = buf[q & 1];
+            tmem_arrived(v);
+            tmem_ld32(ts + 32 * ((q + 1) & 3), buf[(q + 1) & 1]);  // (the first ones again at the end)
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+              const float ks = sc.ks[2 * q + s];
+              if (kMasked) {
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                  const int c = 32 * q + 16 * s + e;
+                  if (c < c_lo || c >= c_hi || ks < 0.0f) v[16 * s + e] = 0xFF800000u;
+                }
+              }
+              float x0 = __uint_as_float(v[16 * s]), x1 = __uint_as_float(v[16 * s + 1]);
+#pragma unroll
+              for (int e = 2; e < 14; e += 4) {
+                x0 = max3(x0, __uint_as_float(v[16 * s + e]), __uint_as_float(v[16 * s + e + 1]));
+                x1 = max3(x1, __uint_as_float(v[16 * s + e + 2]), __uint_as_float(v[16 * s + e + 3]));
+              }
+              x0 = max3(x0, __uint_as_float(v[16 * s + 14]), __uint_as_float(v[16 * s + 15]));
+              // (0 * -inf of a fully hidden segment would be NaN, which fmaxf drops)
+              top = fmaxf(top, __fmaf_rn(fmaxf(x0, x1), fac * fabsf(ks), sc.lv[2 * q + s]));
+            }
+          }
+          // m follows where a score passes it by 2^kLazy (or is the row's
+          // first), in whole steps, so that the row's sum and O are scaled
+          // exactly
+          const bool grow = top > m + kLazy;
+          if (__any_sync(0xffffffffu, grow)) {
+            const float next = grow ? ceilf(top) : m;
+            const float down = fmaxf(m - next, -127.0f);  // m = -inf: f = 0
+            const float f = m == next ? 1.0f : __uint_as_float(static_cast<uint32_t>(127 + static_cast<int>(down)) << 23);
+            m = next;
+            l *= f;
+            if (j > 0) {
+              const bool waited = wait_for(&pv_done[t], (tj - 1) & 1, p.status);
+              if (!__all_sync(0xffffffffu, waited)) return false;
+              tc_fence_after();
+#pragma unroll 1
+              for (int e = 0; e < D / 16; ++e) {
+                uint32_t o[16];
+                tmem_ld16(to + 16 * e, o);
+                tmem_arrived(o);
+#pragma unroll
+                for (int z = 0; z < 16; ++z) o[z] = __float_as_uint(__fmul_rn(__uint_as_float(o[z]), f));
+                tmem_st16(to + 16 * e, o);
+              }
+            }
+          }
+          const float from = m == -INFINITY ? 0.0f : kRaise - m;
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
             uint32_t(&v)[32] = buf[q & 1];
             tmem_arrived(v);
             if (q < 3) tmem_ld32(ts + 32 * (q + 1), buf[(q + 1) & 1]);
-            float top = -INFINITY;
+            uint32_t w[16];
 #pragma unroll
-            for (int s = 0; s < 2; ++s) {  // score + log2 vs, in place
-              const float ks = sc.ks[2 * q + s], lv = sc.lv[2 * q + s];
-              const float c1 = fac * fabsf(ks);
-              const uint64_t c11 = pair(c1, c1), c00 = pair(lv, lv);
-              float top0 = -INFINITY, top1 = -INFINITY;
+            for (int s = 0; s < 2; ++s) {
+              const float ks = sc.ks[2 * q + s];
+              const float c1 = fac * fabsf(ks), c0 = sc.lv[2 * q + s] + from;
+              const uint64_t c11 = pair(c1, c1), c00 = pair(c0, c0);
+              uint64_t sum = pair(0.0f, 0.0f);
 #pragma unroll
               for (int e = 0; e < 8; ++e) {
                 const int at = 16 * s + 2 * e, c = 32 * q + at;
@@ -361,62 +411,6 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_prompt_kernel(const 
                   if (c < c_lo || c >= c_hi || ks < 0.0f) x0 = -INFINITY;
                   if (c + 1 < c_lo || c + 1 >= c_hi || ks < 0.0f) x1 = -INFINITY;
                 }
-                if ((e & 1) != 0)
-                  top1 = max3(top1, x0, x1);
-                else
-                  top0 = max3(top0, x0, x1);
-                v[at] = __float_as_uint(x0);
-                v[at + 1] = __float_as_uint(x1);
-              }
-              top = max3(top, top0, top1);
-            }
-            const bool grow = top > m + kLazy;  // also the first score seen (m = -inf)
-            if (__any_sync(0xffffffffu, grow)) {
-              // (a row that needs it alone; whole steps, so nothing is rounded)
-              const float to_m = grow ? ceilf(top) : m;
-              const float down = fmaxf(m - to_m, -127.0f);  // m = -inf: f = 0
-              const float f = m == to_m ? 1.0f : __uint_as_float(static_cast<uint32_t>(127 + static_cast<int>(down)) << 23);
-              m = to_m;
-              l *= f;
-              tmem_wait_st();  // what is loaded here may have just been stored
-#pragma unroll 1
-              for (int e = 0; e < q; ++e) {
-                uint32_t w[16];
-                tmem_ld16(ts + 16 * e, w);
-                tmem_arrived(w);
-#pragma unroll
-                for (int z = 0; z < 16; ++z) {  // (f may be below what fp16 holds, the product above)
-                  const float2 a = __half22float2(*reinterpret_cast<const __half2 *>(&w[z]));
-                  w[z] = half2_bits(__floats2half2_rn(__fmul_rn(a.x, f), __fmul_rn(a.y, f)));
-                }
-                tmem_st16(ts + 16 * e, w);
-              }
-              if (j > 0) {
-                const bool waited = wait_for(&pv_done[t], (tj - 1) & 1, p.status);
-                if (!__all_sync(0xffffffffu, waited)) return false;
-                tc_fence_after();
-#pragma unroll 1
-                for (int e = 0; e < D / 16; ++e) {
-                  uint32_t o[16];
-                  tmem_ld16(to + 16 * e, o);
-                  tmem_arrived(o);
-#pragma unroll
-                  for (int z = 0; z < 16; ++z) o[z] = __float_as_uint(__fmul_rn(__uint_as_float(o[z]), f));
-                  tmem_st16(to + 16 * e, o);
-                }
-              }
-            }
-            const float from = m == -INFINITY ? 0.0f : kRaise - m;
-            const uint64_t shift = pair(from, from);
-            uint32_t w[16];
-#pragma unroll
-            for (int s = 0; s < 2; ++s) {
-              uint64_t sum = pair(0.0f, 0.0f);
-#pragma unroll
-              for (int e = 0; e < 8; ++e) {
-                const int at = 16 * s + 2 * e;
-                float x0, x1;
-                unpair(add2(pair(__uint_as_float(v[at]), __uint_as_float(v[at + 1])), shift), x0, x1);
                 x0 = ex2(x0);
                 x1 = ex2(x1);
                 sum = add2(sum, pair(x0, x1));
