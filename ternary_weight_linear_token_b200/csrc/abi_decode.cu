@@ -45,7 +45,7 @@ bitnet_status check_batch_sizes(int64_t T, int64_t B, int64_t max_pages, const i
                                 int64_t max_new, const bitnet_kv_cache *cache) {
   if (T < 0 || T > kMaxCount || B < 0 || B > kMaxCount || max_pages < 0 || max_new < 0)
     return BITNET_ERR_INVALID_ARG;
-  if (max_pages > kMaxCount / cache->page_tokens || max_new > kMaxCount) return BITNET_ERR_INVALID_ARG;
+  if (max_pages > (int64_t(1) << 30) / cache->page_tokens || max_new > kMaxCount) return BITNET_ERR_INVALID_ARG;
   if (offsets == nullptr && T != B) return BITNET_ERR_INVALID_ARG;  // one row per sequence
   return BITNET_OK;
 }

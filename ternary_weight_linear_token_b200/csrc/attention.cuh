@@ -16,18 +16,22 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLazy = 8.0f;
 constexpr float kRaise = 7.0f;
 
-// The rows of sequence b and its length; false for numbers that do not
-// describe one.
-__device__ __forceinline__ bool kv_sequence(const KvBatch &batch, int P, int64_t b, int64_t *r0,
-                                         int64_t *r1, int64_t *len) {
-  *len = batch.lens[b];
+// The rows r0 .. r1 - 1 of sequence b and its length; false for numbers that
+// do not describe one.  (Rows of queries and positions fit 32 bits: T *
+// q_heads and max_pages * page_tokens are below 2^31.)
+__device__ __forceinline__ bool kv_sequence(const KvBatch &batch, int P, int b, int *r0, int *r1, int *len) {
+  *len = __ldg(batch.lens + b);
   *r0 = b;
   *r1 = b + 1;
   if (batch.offsets != nullptr) {
-    *r0 = batch.offsets[b];
-    *r1 = batch.offsets[b + 1];
+    *r0 = __ldg(batch.offsets + b);
+    *r1 = __ldg(batch.offsets + b + 1);
   }
   return *r0 >= 0 && *r1 <= batch.T && *r0 <= *r1 && *len >= 0 && *len <= batch.max_pages * P;
+}
+// The first position that a query at `pos` sees.
+__device__ __forceinline__ int first_seen(int pos, int window) {
+  return window > 0 && pos >= window ? pos - window + 1 : 0;
 }
 
 __device__ __forceinline__ float ex2(float x) {

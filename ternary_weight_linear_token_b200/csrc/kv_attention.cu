@@ -49,16 +49,16 @@ struct AttnParams {
   void *o;
   int q_heads, group;
   float scale_log2;
-  int64_t window;
+  int window;
   int row_tiles, pieces;
-  int64_t piece;       // tokens per piece, a multiple of kChunk
+  int piece;           // tokens per piece, a multiple of kChunk
   float *part_o;       // [pieces][T * q_heads][D]; null: one piece, O written here
   float2 *part_ml;     // [pieces][T * q_heads] (max, sum)
   int *status;
 };
 
 template <int D> struct Ring {
-  static constexpr int kStages = D == 128 ? 3 : 6;
+  static constexpr int kStages = D == 128 ? 2 : 4;
   static constexpr int kBytes = kChunk * D;            // K, and V, of a chunk
   static constexpr int kStageBytes = 2 * kBytes;
 };
@@ -73,11 +73,9 @@ template <int D> constexpr size_t attn_smem() {
 
 // Positions that some of the queries i0..i1 of a sequence sees: [lo, hi),
 // lo rounded down to a chunk.
-__device__ __forceinline__ void visible(int64_t len, int64_t n, int64_t i0, int64_t i1,
-                                        int64_t window, int64_t *lo, int64_t *hi) {
+__device__ __forceinline__ void visible(int len, int n, int i0, int i1, int window, int *lo, int *hi) {
   *hi = len - n + i1 + 1;
-  const int64_t first = window > 0 ? len - n + i0 - window + 1 : 0;
-  *lo = (first > 0 ? first : 0) / kChunk * kChunk;
+  *lo = first_seen(len - n + i0, window) / kChunk * kChunk;
 }
 
 __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
@@ -101,15 +99,15 @@ template <typename T> __device__ __forceinline__ T lds(const void *p) { return *
 // One row tile of one piece.  TERMS: columns per query row (1 bf16, 2 fp32);
 // NT: column tiles of 8.
 template <int D, int TERMS, int NT>
-__device__ __forceinline__ void attend(const AttnParams &p, uint8_t *smem, int64_t b, int h,
-                                       int row_tile, int64_t piece_index, int64_t r0, int64_t n,
-                                       int64_t len, uint32_t &phase) {
+__device__ __forceinline__ void attend(const AttnParams &p, uint8_t *smem, int b, int h, int row_tile,
+                                       int piece_index, int r0, int n, int len, uint32_t &phase,
+                                       int &stage) {
   using R = Ring<D>;
   constexpr int kRows = 8 * NT / TERMS;
   constexpr int kSteps = D / 16;     // K steps of S^T; M tiles of O^T
   constexpr int kPer = 2 / TERMS;    // query rows per lane and column tile
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  const int P = p.cache.page_tokens, H = p.cache.heads, G = p.group;
+  const int P = p.cache.page_tokens, G = p.group, page_shift = 31 - __clz(P);
   uint8_t *ring = smem + warp * R::kStages * R::kStageBytes;
   ChunkScales *scales = reinterpret_cast<ChunkScales *>(smem + kWarps * R::kStages * R::kStageBytes) +
                         warp * R::kStages;
@@ -118,55 +116,53 @@ __device__ __forceinline__ void attend(const AttnParams &p, uint8_t *smem, int64
                    warp * R::kStages;
 
   // query rows of the tile: row = query * G + head of the group
-  const int64_t row0 = static_cast<int64_t>(row_tile) * kRows;
-  const int64_t rows = n * G - row0 < kRows ? n * G - row0 : kRows;
-  int64_t lo, hi;
-  visible(len, n, row0 / G, (row0 + rows - 1) / G, p.window, &lo, &hi);
-  lo += piece_index * p.piece;
-  if (hi > lo + p.piece) hi = lo + p.piece;
-  const int64_t chunks = hi > lo ? (hi - lo + kChunk - 1) / kChunk : 0;
+  const int row0 = row_tile * kRows;
+  const int rows = n * G - row0 < kRows ? n * G - row0 : kRows;
+  const int query0 = row0 / G, query1 = (row0 + rows - 1) / G;  // of the first and last row
+  int lo, hi;
+  visible(len, n, query0, query1, p.window, &lo, &hi);
+  if (p.part_o != nullptr) {
+    lo = hi - lo > piece_index * p.piece ? lo + piece_index * p.piece : hi;
+    if (hi - lo > p.piece) hi = lo + p.piece;
+  }
+  const int chunks = hi > lo ? (hi - lo + kChunk - 1) / kChunk : 0;
   if (chunks == 0 && p.part_o != nullptr) return;  // the joining kernel knows
 
-  // The page of a lane's tile of the chunk (lanes 0-3: tile = lane & 1, K or
-  // V = lane >> 1); -1 where there is none.
-  const int *table = p.batch.pages + b * p.batch.max_pages;
-  auto page_of = [&](int64_t c) -> int {
-    const int64_t tok = lo + c * kChunk + 16 * (lane & 1);
-    return (lane < 4 && c < chunks && tok < hi) ? __ldg(table + tok / P) : -1;
+  // Lanes 0-3 fetch the chunk of the warp's round i (tile = lane & 1, K or V =
+  // lane >> 1): the page number (-1 where there is none), ...
+  const int *table = p.batch.pages + static_cast<int64_t>(b) * p.batch.max_pages;
+  const int64_t page_bytes = static_cast<int64_t>(p.cache.heads) * P * D;
+  const int8_t *codes = (lane >> 1 ? p.cache.v_codes : p.cache.k_codes) + static_cast<int64_t>(h) * P * D;
+  const float *page_scales = (lane >> 1 ? p.cache.v_scales : p.cache.k_scales) + h;
+  const int tok_lane = lo + warp * kChunk + 16 * (lane & 1);
+  const int rounds = (chunks - warp + kWarps - 1) / kWarps;
+  auto page_of = [&](int i) -> int {
+    const int tok = tok_lane + i * (kWarps * kChunk);
+    return lane < 4 && i < rounds && tok < hi ? __ldg(table + (tok >> page_shift)) : -1;
   };
-  auto good_page = [&](int page, int64_t c) -> bool {
-    const int64_t tok = lo + c * kChunk + 16 * (lane & 1);
-    if (lane >= 4 || c >= chunks || tok >= hi) return false;
-    if (page >= 0 && page < p.cache.pages) return true;
-    record_status(p.status, kStatusRange);
-    return false;
-  };
-  // Lanes 0-3 copy their tile (pages of 32 tokens and more: the chunk's first
-  // lane copies both tiles' bytes).
-  auto issue = [&](int64_t c, int page) -> float {
-    const int st = static_cast<int>((c / kWarps) % R::kStages);
-    const bool ok = good_page(page, c);
-    const int64_t tok = lo + c * kChunk + 16 * (lane & 1);
-    const unsigned pair = __ballot_sync(0xffffffffu, ok);
-    const bool whole = P >= kChunk;  // both tiles in one page
-    const uint32_t bytes = whole ? R::kBytes : R::kBytes / 2;
-    const unsigned copies = whole ? pair & 5u : pair & 15u;
+  // ... then its bytes into stage st (pages of 32 tokens and more: the first
+  // tile's lanes copy both tiles), and its scale, -1 where there is no page.
+  const bool whole = P >= kChunk;
+  const uint32_t bytes = whole ? R::kBytes : R::kBytes / 2;
+  auto issue = [&](int i, int page, int st) -> float {
+    const int tok = tok_lane + i * (kWarps * kChunk);
+    const bool wanted = lane < 4 && tok < hi;
+    const bool ok = wanted && page >= 0 && page < p.cache.pages;
+    if (wanted && !ok) record_status(p.status, kStatusRange);
+    const unsigned copies = __ballot_sync(0xffffffffu, ok) & (whole ? 5u : 15u);
     if (lane == 0) mbar_arrive_expect_tx(&full[st], bytes * __popc(copies));
     __syncwarp();
-    float s = -1.0f;  // no page
+    float s = -1.0f;
     if (ok) {
-      const int64_t head = static_cast<int64_t>(page) * H + h;
-      s = __ldg((lane >> 1 ? p.cache.v_scales : p.cache.k_scales) + head);
-      if ((copies >> lane) & 1u) {
-        const int8_t *src = (lane >> 1 ? p.cache.v_codes : p.cache.k_codes) + (head * P + tok % P) * D;
+      s = __ldg(page_scales + static_cast<int64_t>(page) * p.cache.heads);
+      if ((copies >> lane) & 1u)
         bulk_g2s(ring + st * R::kStageBytes + (lane >> 1) * R::kBytes + (lane & 1) * (R::kBytes / 2),
-                 src, bytes, &full[st]);
-      }
+                 codes + page * page_bytes + (tok & (P - 1)) * D, bytes, &full[st]);
     }
     return s;
   };
-  auto keep_scale = [&](int64_t c, float s) {
-    ChunkScales &k = scales[(c / kWarps) % R::kStages];
+  auto keep_scale = [&](int st, float s) {
+    ChunkScales &k = scales[st];
     if (lane < 2) k.ks[lane] = s;
     if (lane == 2 || lane == 3) {
       // s = 0: a page of zeros; s < 0: no page, its tokens are not seen
@@ -177,24 +173,31 @@ __device__ __forceinline__ void attend(const AttnParams &p, uint8_t *smem, int64
   };
 
   // ring: the first kStages chunks of this warp
-  int next_page = page_of(warp);
-  for (int i = 0; i < R::kStages; ++i) {
-    const int64_t c = warp + static_cast<int64_t>(i) * kWarps;
-    if (c >= chunks) break;
-    const int page = next_page;
-    next_page = page_of(c + kWarps);
-    keep_scale(c, issue(c, page));
+  int next_page;
+  {
+    int page[R::kStages];
+    float s[R::kStages];
+#pragma unroll
+    for (int i = 0; i < R::kStages; ++i) page[i] = page_of(i);
+    next_page = page_of(R::kStages);
+#pragma unroll
+    for (int i = 0; i < R::kStages; ++i)
+      if (i < rounds) s[i] = issue(i, page[i], (stage + i) % R::kStages);
+#pragma unroll
+    for (int i = 0; i < R::kStages; ++i)
+      if (i < rounds) keep_scale((stage + i) % R::kStages, s[i]);
   }
 
   // q as B fragments: column g of column tile j is row j * 8 / TERMS + g / TERMS
   uint32_t qf[NT][kSteps][2];
   float fac[NT][kPer];     // score factor of the lane's rows (columns 2t, 2t + 1)
-  int64_t pos[NT][kPer];   // their positions; -1: no such row
+  int pos[NT][kPer], first[NT][kPer];  // the last and first positions they see; no such row: -1, 0
 #pragma unroll
   for (int j = 0; j < NT; ++j) {
-    const int64_t row = row0 + j * (8 / TERMS) + g / TERMS;
+    const int row = row0 + j * (8 / TERMS) + g / TERMS, query = row / G;
     const bool have = row < row0 + rows;
-    const int64_t at = ((r0 + row / G) * p.q_heads + static_cast<int64_t>(h) * G + row % G) * D;
+    const int64_t at = (static_cast<int64_t>(r0 + query) * p.q_heads + h * G + (row - query * G)) * D;
+    const int place = have ? len - n + query : -1;
     float v[D / 4];
     float peak = 0.0f;
 #pragma unroll
@@ -242,8 +245,8 @@ __device__ __forceinline__ void attend(const AttnParams &p, uint8_t *smem, int64
     for (int r = 0; r < kPer; ++r) {
       const int col = 2 * t + r;
       fac[j][r] = __shfl_sync(0xffffffffu, f, col * 4);
-      const int64_t mine = row0 + j * (8 / TERMS) + col / TERMS;
-      pos[j][r] = mine < row0 + rows ? len - n + mine / G : -1;
+      pos[j][r] = __shfl_sync(0xffffffffu, place, col * 4);
+      first[j][r] = first_seen(pos[j][r], p.window);
     }
   }
 
@@ -263,18 +266,19 @@ __device__ __forceinline__ void attend(const AttnParams &p, uint8_t *smem, int64
   }
   // positions that every row of the tile sees need no mask
   // (columns past the last row hold zeros and are not stored)
-  const int64_t all_hi = len - n + row0 / G + 1;
-  const int64_t all_lo = p.window > 0 ? len - n + (row0 + rows - 1) / G - p.window + 1 : 0;
+  const int all_hi = len - n + query0 + 1, all_lo = first_seen(len - n + query1, p.window);
 
   __syncwarp();
-  for (int64_t c = warp; c < chunks; c += kWarps) {
-    const int st = static_cast<int>((c / kWarps) % R::kStages);
-    const bool ok = mbar_wait(&full[st], (phase >> st) & 1u, p.status);
+#pragma unroll 1
+  for (int i = 0; i < rounds; ++i) {
+    const int st = stage;
+    stage = stage + 1 == R::kStages ? 0 : stage + 1;
+    const bool ok = wait_for(&full[st], (phase >> st) & 1u, p.status);
     if (!__all_sync(0xffffffffu, ok)) break;
     phase ^= 1u << st;
     const uint8_t *kt = ring + st * R::kStageBytes;
     const uint8_t *vt = kt + R::kBytes;
-    const int64_t tok0 = lo + c * kChunk;
+    const int tok0 = lo + (i * kWarps + warp) * kChunk;
 
     // ---- scores (log2) of the chunk's two tiles: [tile][j][row of lane][token g, g + 8]
     float s2[2][NT][kPer][2];
@@ -300,8 +304,6 @@ __device__ __forceinline__ void attend(const AttnParams &p, uint8_t *smem, int64
         }
       }
       const float ks = scales[st].ks[tile], lv = scales[st].lv[tile];
-      const int64_t tok = tok0 + 16 * tile;
-      const bool masked = tok + 16 > all_hi || tok < all_lo || tok + 16 > hi || ks < 0.0f;
 #pragma unroll
       for (int j = 0; j < NT; ++j)
 #pragma unroll
@@ -309,14 +311,29 @@ __device__ __forceinline__ void attend(const AttnParams &p, uint8_t *smem, int64
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
             const float x = TERMS == 2 ? sc[j][2 * e] + sc[j][2 * e + 1] : sc[j][2 * e + r];
-            float y = __fmaf_rn(x, ks * fac[j][r], lv);
-            if (masked) {
-              const int64_t at = tok + g + 8 * e;
-              const bool seen = ks >= 0.0f && at <= pos[j][r] && at < hi && (p.window <= 0 || at > pos[j][r] - p.window);
-              if (!seen) y = -INFINITY;
-            }
-            s2[tile][j][r][e] = y;
+            s2[tile][j][r][e] = __fmaf_rn(x, ks * fac[j][r], lv);
           }
+    }
+    // not seen by all rows: compare (one branch for the chunk)
+    if (tok0 + kChunk > all_hi || tok0 < all_lo || tok0 + kChunk > hi || scales[st].ks[0] < 0.0f ||
+        scales[st].ks[1] < 0.0f) {
+#pragma unroll 1
+      for (int tile = 0; tile < 2; ++tile) {
+        const int at = tok0 + 16 * tile + g;
+        const bool there = !(scales[st].ks[tile] < 0.0f);
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+          for (int r = 0; r < kPer; ++r)
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+              if (!(there && at + 8 * e <= pos[j][r] && at + 8 * e >= first[j][r] && at + 8 * e < hi)) {
+                if (tile == 0)
+                  s2[0][j][r][e] = -INFINITY;
+                else
+                  s2[1][j][r][e] = -INFINITY;
+              }
+      }
     }
 
     // ---- running maximum
@@ -416,11 +433,11 @@ __device__ __forceinline__ void attend(const AttnParams &p, uint8_t *smem, int64
 
     // ---- refill this stage
     __syncwarp();  // every lane has read it
-    const int64_t nc = c + static_cast<int64_t>(kWarps) * R::kStages;
-    if (nc < chunks) {
+    const int ahead = i + R::kStages;
+    if (ahead < rounds) {
       const int page = next_page;
-      next_page = page_of(nc + kWarps);
-      keep_scale(nc, issue(nc, page));
+      next_page = page_of(ahead + 1);
+      keep_scale(st, issue(ahead, page, st));
       __syncwarp();
     }
   }
@@ -472,10 +489,10 @@ __device__ __forceinline__ void attend(const AttnParams &p, uint8_t *smem, int64
       y = __fmaf_rn(f, v.y, y);
       sum = __fmaf_rn(f, ml.y, sum);
     }
-    const int64_t gr = row0 + row;
-    const int64_t out_row = (r0 + gr / G) * p.q_heads + static_cast<int64_t>(h) * G + gr % G;
+    const int query = (row0 + row) / G;
+    const int64_t out_row = static_cast<int64_t>(r0 + query) * p.q_heads + h * G + (row0 + row - query * G);
     if (p.part_o != nullptr) {
-      const int64_t at = piece_index * p.batch.T * p.q_heads + out_row;
+      const int64_t at = static_cast<int64_t>(piece_index) * p.batch.T * p.q_heads + out_row;
       *reinterpret_cast<float2 *>(p.part_o + at * D + d) = make_float2(x, y);
       if (d == 0) p.part_ml[at] = make_float2(top, sum);
     } else {
@@ -490,7 +507,7 @@ __device__ __forceinline__ void attend(const AttnParams &p, uint8_t *smem, int64
 }
 
 template <int D, int TERMS, int NT>
-__global__ void __launch_bounds__(kWarps * 32, 2) kv_attention_kernel(const AttnParams p) {
+__global__ void __launch_bounds__(kWarps * 32, 3) kv_attention_kernel(const AttnParams p) {
   extern __shared__ __align__(128) uint8_t smem[];
   using R = Ring<D>;
   uint64_t *full = reinterpret_cast<uint64_t *>(
@@ -502,22 +519,23 @@ __global__ void __launch_bounds__(kWarps * 32, 2) kv_attention_kernel(const Attn
   pdl_launch_dependents();
   constexpr int kRows = 8 * NT / TERMS;
   // piece fastest, then head, row tile, sequence
-  int64_t i = blockIdx.x;
-  const int64_t piece = i % p.pieces;
+  unsigned i = blockIdx.x;
+  const int piece = static_cast<int>(i % p.pieces);
   i /= p.pieces;
   const int h = static_cast<int>(i % p.cache.heads);
   i /= p.cache.heads;
   const int first_tile = static_cast<int>(i % p.row_tiles);
-  const int64_t b = i / p.row_tiles;
-  int64_t r0, r1, len;
+  const int b = static_cast<int>(i / p.row_tiles);
+  int r0, r1, len;
   if (!kv_sequence(p.batch, p.cache.page_tokens, b, &r0, &r1, &len)) {
     if (threadIdx.x == 0) record_status(p.status, kStatusRange);
     return;
   }
-  const int64_t n = r1 - r0, tiles = (n * p.group + kRows - 1) / kRows;
+  const int n = r1 - r0, tiles = (n * p.group + kRows - 1) / kRows;
   uint32_t phase = 0;  // bit s: the parity of the warp's stage s to wait for next
-  for (int64_t rt = first_tile; rt < tiles; rt += p.row_tiles) {
-    attend<D, TERMS, NT>(p, smem, b, h, static_cast<int>(rt), piece, r0, n, len, phase);
+  int stage = 0;       // its next stage
+  for (int rt = first_tile; rt < tiles; rt += p.row_tiles) {
+    attend<D, TERMS, NT>(p, smem, b, h, rt, piece, r0, n, len, phase, stage);
     fence_proxy_async_smem();  // the joined sums lie where the next bulk copies go
     __syncthreads();
   }
@@ -526,70 +544,86 @@ __global__ void __launch_bounds__(kWarps * 32, 2) kv_attention_kernel(const Attn
 // Joins the pieces of one query row (a CTA each), in piece order.
 template <int D, bool F32>
 __global__ void __launch_bounds__(kWarps * 32) kv_join_kernel(const AttnParams p, int rows_per_tile) {
-  __shared__ int64_t seq[4];
+  __shared__ int seq;
   __shared__ float so[kWarps][D];
-  __shared__ float2 sml[kWarps];
+  __shared__ float weight[kWarps * 32], tops[kWarps], sums[kWarps];
   pdl_wait();
   pdl_launch_dependents();
-  const int64_t row = blockIdx.x;               // token * q_heads + head
-  const int64_t t = row / p.q_heads;
+  const int row = blockIdx.x;               // token * q_heads + head
+  const int t = row / p.q_heads;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (threadIdx.x == 0) seq[0] = -1;
-  __syncthreads();
-  if (p.batch.offsets == nullptr) {
-    if (threadIdx.x == 0) seq[0] = t;
-  } else {
-    for (int64_t b = threadIdx.x; b < p.batch.B; b += blockDim.x)
-      if (p.batch.offsets[b] <= t && t < p.batch.offsets[b + 1]) seq[0] = b;
+  int b = t;
+  if (p.batch.offsets != nullptr) {
+    if (threadIdx.x == 0) seq = -1;
+    __syncthreads();
+    for (int i = threadIdx.x; i < p.batch.B; i += kWarps * 32)
+      if (p.batch.offsets[i] <= t && t < p.batch.offsets[i + 1]) seq = i;
+    __syncthreads();
+    b = seq;
+    if (b < 0) return;  // a row of no sequence: left as it is
   }
-  __syncthreads();
-  const int64_t b = seq[0];
-  if (b < 0) return;  // a row of no sequence: left as it is
-  int64_t r0, r1, len;
+  int r0, r1, len;
   if (!kv_sequence(p.batch, p.cache.page_tokens, b, &r0, &r1, &len)) return;
-  const int64_t n = r1 - r0;
-  const int64_t in = (t - r0) * p.group + row % p.q_heads % p.group;
-  const int64_t row0 = in / rows_per_tile * rows_per_tile;
-  const int64_t last = row0 + rows_per_tile < n * p.group ? row0 + rows_per_tile : n * p.group;
-  int64_t lo, hi;
+  const int n = r1 - r0;
+  const int in = (t - r0) * p.group + row % p.q_heads % p.group;
+  const int row0 = in / rows_per_tile * rows_per_tile;
+  const int last = row0 + rows_per_tile < n * p.group ? row0 + rows_per_tile : n * p.group;
+  int lo, hi;
   visible(len, n, row0 / p.group, (last - 1) / p.group, p.window, &lo, &hi);
-  int64_t pieces = hi > lo ? (hi - lo + p.piece - 1) / p.piece : 0;
+  int pieces = hi > lo ? (hi - lo + p.piece - 1) / p.piece : 0;
   if (pieces > p.pieces) pieces = p.pieces;
 
+  // weights of 128 pieces at a time (their maxima and sums fetched together),
+  // then their rows, a warp every 4th, several in flight
   constexpr int kPer = D / 32;
+  const int64_t stride = p.batch.T * p.q_heads;
   float top = -INFINITY, sum = 0.0f, x[kPer];
 #pragma unroll
   for (int e = 0; e < kPer; ++e) x[e] = 0.0f;
-  for (int64_t i = warp; i < pieces; i += kWarps) {
-    const int64_t at = i * p.batch.T * p.q_heads + row;
-    const float2 ml = p.part_ml[at];
-    float v[kPer];
+  for (int i0 = 0; i0 < pieces; i0 += kWarps * 32) {
+    const int mine = i0 + threadIdx.x;
+    const float2 ml = mine < pieces ? p.part_ml[mine * stride + row] : make_float2(-INFINITY, 0.0f);
+    __syncthreads();  // the last round's weights have been read
+    const unsigned key = __float_as_uint(ml.x);  // (order of floats as integers, NaN aside)
+    const int ordered = static_cast<int>(key ^ ((key >> 31) != 0 ? 0x7FFFFFFFu : 0u));
+    const int best = __reduce_max_sync(0xffffffffu, ordered);
+    if (lane == 0) tops[warp] = __uint_as_float(static_cast<unsigned>(best) ^ (best < 0 ? 0x7FFFFFFFu : 0u));
+    __syncthreads();
+    float to = top;
 #pragma unroll
-    for (int e = 0; e < kPer; ++e) v[e] = p.part_o[at * D + lane * kPer + e];
-    if (ml.x == -INFINITY && ml.y == 0.0f) continue;  // (a NaN sum goes on)
-    const float to = fmaxf(top, ml.x);
-    const float f = top == -INFINITY ? 0.0f : ex2(top - to), a = ex2(ml.x - to);
-    sum = __fmaf_rn(sum, f, ml.y * a);
+    for (int w = 0; w < kWarps; ++w) to = fmaxf(to, tops[w]);
+    const float old = top == -INFINITY ? 0.0f : ex2(top - to);
+    // (a piece without a maximum has a sum of 0, or of NaN, which goes on)
+    const float f = ml.x == -INFINITY ? (ml.y == 0.0f ? 0.0f : ml.y) : ex2(ml.x - to);
+    weight[threadIdx.x] = f;
+    __syncthreads();
+    float part = f * ml.y;
 #pragma unroll
-    for (int e = 0; e < kPer; ++e) x[e] = __fmaf_rn(x[e], f, v[e] * a);
+    for (int o = 16; o > 0; o >>= 1) part += __shfl_xor_sync(0xffffffffu, part, o);
+    sum = __fmaf_rn(sum, old, part);  // of this warp's pieces
     top = to;
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) x[e] *= old;
+    const int n_here = pieces - i0 < kWarps * 32 ? pieces - i0 : kWarps * 32;
+#pragma unroll 4
+    for (int i = warp; i < n_here; i += kWarps) {
+      const float *src = p.part_o + ((i0 + i) * stride + row) * D + lane * kPer;
+#pragma unroll
+      for (int e = 0; e < kPer; ++e) x[e] = __fmaf_rn(weight[i], src[e], x[e]);
+    }
   }
 #pragma unroll
   for (int e = 0; e < kPer; ++e) so[warp][lane * kPer + e] = x[e];
-  if (lane == 0) sml[warp] = make_float2(top, sum);
+  if (lane == 0) sums[warp] = sum;
   __syncthreads();
   for (int d = threadIdx.x; d < D; d += kWarps * 32) {
-    float all = -INFINITY;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) all = fmaxf(all, sml[w].x);
     float y = 0.0f, z = 0.0f;
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
-      const float f = sml[w].x == -INFINITY ? 0.0f : ex2(sml[w].x - all);
-      y = __fmaf_rn(f, so[w][d], y);
-      z = __fmaf_rn(f, sml[w].y, z);
+      y += so[w][d];
+      z += sums[w];
     }
-    const float out = z == 0.0f ? 0.0f : __fdiv_rn(y, z);
+    const float out = z == 0.0f ? 0.0f : __fdiv_rn(y, z);  // nothing visible: zeros
     if (F32)
       static_cast<float *>(p.o)[row * D + d] = out;
     else
@@ -614,13 +648,13 @@ AttnPlan plan_of(const KvCache &cache, const KvBatch &batch, const AttnArgs &arg
   int64_t span = batch.max_pages * cache.page_tokens;
   if (args.window > 0 && args.window + a.rows + kChunk < span) span = args.window + a.rows + kChunk;
   const int64_t units = batch.B * cache.heads * a.row_tiles;
-  const int64_t target = kSms * 8;
+  const int64_t target = kSms * 5;
   int64_t piece = ceil_div(ceil_div(span * units, target), 128) * 128;
   if (piece < 128) piece = 128;
   a.pieces = ceil_div(span, piece);
   if (a.pieces <= 1 || units >= target) {
     a.pieces = 1;
-    piece = (int64_t(1) << 40);
+    piece = (int64_t(1) << 30);
   }
   a.piece = piece;
   return a;
@@ -662,7 +696,7 @@ bool kv_attention_fits(const KvCache &cache, const KvBatch &batch, const AttnArg
   const int64_t most = (int64_t(1) << 31) - 1;
   return a.row_tiles <= most && batch.B * a.row_tiles <= most / cache.heads &&
          batch.B * a.row_tiles * cache.heads <= most / a.pieces &&
-         (a.pieces == 1 || batch.T <= most / args.q_heads);
+         batch.T <= (most - 512) / args.q_heads;
 }
 
 cudaError_t launch_kv_attention(const KvCache &cache, const KvBatch &batch, const AttnArgs &args,
@@ -677,10 +711,10 @@ cudaError_t launch_kv_attention(const KvCache &cache, const KvBatch &batch, cons
   p.q_heads = args.q_heads;
   p.group = args.q_heads / cache.heads;
   p.scale_log2 = args.scale * kLog2e;
-  p.window = args.window;
+  p.window = static_cast<int>(args.window < (int64_t(1) << 31) - 1 ? args.window : (int64_t(1) << 31) - 1);
   p.row_tiles = static_cast<int>(a.row_tiles);
   p.pieces = static_cast<int>(a.pieces);
-  p.piece = a.piece;
+  p.piece = static_cast<int>(a.piece);
   p.status = ctx.status;
   if (a.pieces > 1) {
     const size_t rows = static_cast<size_t>(a.pieces) * batch.T * args.q_heads;

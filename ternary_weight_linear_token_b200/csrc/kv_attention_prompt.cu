@@ -55,7 +55,7 @@ struct PromptParams {
   int q_heads, group;
   float scale_log2;     // >= 0; a negative scale turns q's sign
   bool negate;
-  int64_t window;
+  int window;
   int row_blocks;       // of 256 rows, per sequence; a sequence with more strides over them
   int *status;
 };
@@ -210,16 +210,16 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_prompt_kernel(const 
 
   // the last row block of every sequence first (the longest under a causal
   // mask), then the one before it, ...
-  int64_t i = blockIdx.x;
+  unsigned i = blockIdx.x;
   const int h = static_cast<int>(i % p.cache.heads);
   i /= p.cache.heads;
-  const int64_t b = i % p.batch.B;
+  const int b = static_cast<int>(i % p.batch.B);
   const int from_end = static_cast<int>(i / p.batch.B);
   const int P = p.cache.page_tokens, G = p.group;
-  int64_t r0, r1, len;
+  int r0, r1, len;
   const bool fine = kv_sequence(p.batch, P, b, &r0, &r1, &len);
   if (!fine && threadIdx.x == 0) record_status(p.status, kStatusRange);
-  const int64_t n = r1 - r0, blocks = fine ? (n * G + 2 * kTile - 1) / (2 * kTile) : 0;
+  const int n = r1 - r0, blocks = fine ? (n * G + 2 * kTile - 1) / (2 * kTile) : 0;
 
   // KV blocks that this CTA has been through, all in all and of each tile: the
   // counters of the stages' and tiles' barriers
@@ -227,21 +227,17 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_prompt_kernel(const 
   // Positions that rows of row block rb see: [lo, hi), lo on a block boundary;
   // KV blocks of each tile (0: no rows, or none that see anything).  (A table
   // holds less than 2^31 positions.)
-  int lo, hi, nb[2], total;
-  int64_t row0;
-  auto enter = [&](int64_t rb) {
+  int lo, hi, nb[2], total, row0;
+  auto enter = [&](int rb) {
     row0 = rb * 2 * kTile;
-    lo = hi = 0;
-    if (p.window > 0) {
-      const int64_t from = len - n + row0 / G - p.window + 1;
-      lo = static_cast<int>(from > 0 ? from : 0) / kTile * kTile;
-    }
+    hi = 0;
+    lo = first_seen(len - n + row0 / G, p.window) / kTile * kTile;
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
-      const int64_t first = row0 + t * kTile, last = first + kTile < n * G ? first + kTile : n * G;
+      const int first = row0 + t * kTile, last = first + kTile < n * G ? first + kTile : n * G;
       nb[t] = 0;
       if (first < last) {
-        const int end = static_cast<int>(len - n + (last - 1) / G + 1);
+        const int end = len - n + (last - 1) / G + 1;
         if (end > lo) nb[t] = (end - lo + kTile - 1) / kTile;
         if (end > hi) hi = end;
       }
@@ -263,16 +259,16 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_prompt_kernel(const 
 
   if (warp < kConvWarp0) {
     more_registers<kRegsSoftmax>();
-    for (int64_t rb = blocks - 1 - from_end; rb >= 0 && ok; rb -= p.row_blocks) {
+    for (int rb = blocks - 1 - from_end; rb >= 0 && ok; rb -= p.row_blocks) {
       enter(rb);
       // ================================================ softmax
       const int t = warp >> 2, row = threadIdx.x & (kTile - 1);
       const int mine = t ? nb[1] : nb[0];
       const uint32_t before = t ? tiles_done[1] : tiles_done[0];
-      const int64_t gr = row0 + t * kTile + row;
+      const int gr = row0 + t * kTile + row;
       const bool have = gr < n * G;
-      const int64_t query = (have ? gr : n * G - 1) / G;
-      const int64_t at = (have ? (r0 + gr / G) * p.q_heads + static_cast<int64_t>(h) * G + gr % G : 0) * D;
+      const int query = (have ? gr : n * G - 1) / G;
+      const int64_t at = have ? (static_cast<int64_t>(r0 + query) * p.q_heads + h * G + (gr - query * G)) * D : 0;
       // q to shared memory, its largest value brought to [2^14, 2^15)
       float fac;
       {
@@ -313,8 +309,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_prompt_kernel(const 
       }
       const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;  // 32 lanes per warp, bits 16 and up
       const uint32_t ts = tmem + lanes + t * kTile, to = tmem + lanes + 2 * kTile + t * D;
-      const int pos = static_cast<int>(len - n + query);
-      const int first = p.window > 0 && pos - p.window + 1 > 0 ? static_cast<int>(pos - p.window + 1) : 0;
+      const int pos = len - n + query, first = first_seen(pos, p.window);
       float m = -INFINITY, l = 0.0f;  // m is whole
       for (int j = 0; j < mine && ok; ++j) {
         const int slot = static_cast<int>((done + j) % kSlots);
@@ -468,7 +463,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_prompt_kernel(const 
     fewer_registers<kRegsConvert>();
     const bool keys = warp < kValueWarp0;
     const int id = (warp & 3) * 32 + lane;  // thread of the group
-    const int *table = p.batch.pages + b * p.batch.max_pages;
+    const int *table = p.batch.pages + static_cast<int64_t>(b) * p.batch.max_pages;
     const int64_t page_bytes = static_cast<int64_t>(p.cache.heads) * P * D;
     const int8_t *head = (keys ? p.cache.k_codes : p.cache.v_codes) + static_cast<int64_t>(h) * P * D;
     const int page_shift = 31 - __clz(P);
@@ -487,7 +482,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_prompt_kernel(const 
       const int row = (j * kTile + r) & (P - 1);  // (lo is a multiple of every page size)
       return __ldg(reinterpret_cast<const uint4 *>(head + page * page_bytes + row * D) + chunk);
     };
-    for (int64_t rb = blocks - 1 - from_end; rb >= 0 && ok; rb -= p.row_blocks) {
+    for (int rb = blocks - 1 - from_end; rb >= 0 && ok; rb -= p.row_blocks) {
       enter(rb);
       int page = checked(page_of(0), 0), next = page_of(1);
       if (keys) {
@@ -609,7 +604,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_prompt_kernel(const 
   } else {
     fewer_registers<kRegsMma>();
     uint32_t q_phase = 0;
-    for (int64_t rb = blocks - 1 - from_end; rb >= 0 && ok; rb -= p.row_blocks) {
+    for (int rb = blocks - 1 - from_end; rb >= 0 && ok; rb -= p.row_blocks) {
       enter(rb);
       if (warp == kMmaWarp && lane == 0) {
         // ================================================ MMAs
@@ -675,7 +670,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_prompt_kernel(const 
 bool kv_attention_prompt_fits(const KvCache &cache, const KvBatch &batch, const AttnArgs &args) {
   const int64_t most = (int64_t(1) << 31) - 1;
   const int64_t row_blocks = ceil_div(args.max_new * (args.q_heads / cache.heads), 2 * kTile);
-  return row_blocks <= most / cache.heads && batch.B <= most / (row_blocks * cache.heads);
+  return batch.T <= (most - 512) / args.q_heads && row_blocks <= most / cache.heads && batch.B <= most / (row_blocks * cache.heads);
 }
 
 cudaError_t launch_kv_attention_prompt(const KvCache &cache, const KvBatch &batch, const AttnArgs &args,
@@ -689,7 +684,7 @@ cudaError_t launch_kv_attention_prompt(const KvCache &cache, const KvBatch &batc
   p.group = args.q_heads / cache.heads;
   p.negate = args.scale < 0.0f;
   p.scale_log2 = (p.negate ? -args.scale : args.scale) * kLog2e;
-  p.window = args.window;
+  p.window = static_cast<int>(args.window < (int64_t(1) << 31) - 1 ? args.window : (int64_t(1) << 31) - 1);
   p.row_blocks = static_cast<int>(ceil_div(args.max_new * p.group, 2 * kTile));
   p.status = ctx.status;
   const dim3 grid(static_cast<unsigned>(batch.B * p.row_blocks * cache.heads));
