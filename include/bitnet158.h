@@ -524,16 +524,13 @@ bitnet_status bitnet_quantize_weights_w4(const void *W, bitnet_dtype w_dtype, in
 
 /* Y [M][N] = X [M][K] times the transpose of those weights; X and Y fp32 or
  * bf16 each, 16-byte aligned, not overlapping.  Codes are exact, sums fp32.
- * fp32 X runs as three bf16 terms (24 bits; values of bf16's exponent range)
- * and needs a workspace of bitnet_w4a16_matmul_workspace_size bytes (256-byte
- * aligned; 0 for bf16 X).  flags: 0 or BITNET_FLAG_WEIGHTS_STATIC (packed and
- * scales are not written by the kernel before this call).  Made for few
- * tokens; more run in blocks that read the weights again. */
-size_t bitnet_w4a16_matmul_workspace_size(int64_t M, int64_t N, int64_t K, bitnet_dtype x_dtype);
+ * X is finite; fp32 X runs as three bf16 terms (24 bits).  flags: 0 or
+ * BITNET_FLAG_WEIGHTS_STATIC (packed and scales are not written by the kernel
+ * before this call).  Made for few tokens; more run in blocks of 32 that read
+ * the weights again (M at most 8 * 65535). */
 bitnet_status bitnet_w4a16_matmul(const void *X, bitnet_dtype x_dtype, const uint8_t *packed,
                                   const void *scales, int64_t M, int64_t N, int64_t K, int32_t group, void *Y,
-                                  bitnet_dtype y_dtype, void *workspace, size_t workspace_bytes, uint32_t flags,
-                                  bitnet_stream_t stream);
+                                  bitnet_dtype y_dtype, uint32_t flags, bitnet_stream_t stream);
 
 /* ----------------------------------------------------------------------
  * Log probabilities from logits.

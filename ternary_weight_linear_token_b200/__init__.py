@@ -100,9 +100,7 @@ _SIGS["bitnet_kv_attention_workspace_size"] = ([_P, _ST, _I64, _I32, _I64, _I64,
 _SIGS["bitnet_kv_attention"] = ([_P, _P, _P, _ST, _I64, _I32, _P, _I64, _P, _P, _I64, _I64, C.c_float, _I64,
                                  _P, _SZ, _P], _ST)
 _SIGS["bitnet_quantize_weights_w4"] = ([_P, _ST, _I64, _I64, _I32, _P, _P, _P], _ST)
-_SIGS["bitnet_w4a16_matmul_workspace_size"] = ([_I64, _I64, _I64, _ST], _SZ)
-_SIGS["bitnet_w4a16_matmul"] = ([_P, _ST, _P, _P, _I64, _I64, _I64, _I32, _P, _ST, _P, _SZ, C.c_uint32, _P],
-                                _ST)
+_SIGS["bitnet_w4a16_matmul"] = ([_P, _ST, _P, _P, _I64, _I64, _I64, _I32, _P, _ST, C.c_uint32, _P], _ST)
 _SIGS["bitnet_token_logprobs"] = ([_P, _ST, _I64, _I64, _I64, _P, _I32, _P, _P, _P, _P, _P], _ST)
 
 for _name, (_args, _res) in _SIGS.items():
@@ -717,19 +715,9 @@ def bitnet_quantize_weights_w4(W: torch.Tensor, group: int = 128, packed: torch.
     return packed, scales
 
 
-def bitnet_w4a16_matmul_workspace_size(M: int, N: int, K: int, x_dtype: torch.dtype) -> int:
-    return _w4_workspace(int(M), int(N), int(K), _FLOAT[x_dtype])
-
-
-@functools.lru_cache(maxsize=1024)
-def _w4_workspace(M, N, K, kind):
-    return lib.bitnet_w4a16_matmul_workspace_size(M, N, K, kind)
-
-
 def bitnet_w4a16_matmul(X: torch.Tensor, packed: torch.Tensor, scales: torch.Tensor,
                         out_dtype: torch.dtype = torch.bfloat16, Y: torch.Tensor | None = None,
-                        workspace: torch.Tensor | None = None, weights_static: bool = False,
-                        stream=None) -> torch.Tensor:
+                        weights_static: bool = False, stream=None) -> torch.Tensor:
     """Y [M, N] = X [M, K] (fp32/bf16) times the transpose of the 4-bit
     weights of ``bitnet_quantize_weights_w4``; Y fp32/bf16.  Made for few
     tokens (a decode step); more run in blocks."""
@@ -751,7 +739,7 @@ def bitnet_w4a16_matmul(X: torch.Tensor, packed: torch.Tensor, scales: torch.Ten
     if d < 0 or not (d == packed.get_device() == scales.get_device()):
         _same_device(d, packed=packed, scales=scales)
     if stream is not None or d != _current_device():
-        return _elsewhere(d, stream, bitnet_w4a16_matmul, X, packed, scales, out_dtype, Y, workspace,
+        return _elsewhere(d, stream, bitnet_w4a16_matmul, X, packed, scales, out_dtype, Y,
                           weights_static)
     if Y is None:
         Y = X.new_empty((M, N)) if out_dtype is X.dtype else torch.empty((M, N), dtype=out_dtype, device=X.device)
@@ -762,17 +750,8 @@ def bitnet_w4a16_matmul(X: torch.Tensor, packed: torch.Tensor, scales: torch.Ten
     y_kind = _FLOAT.get(Y.dtype)
     if y_kind is None:
         raise TypeError(f"Y must be fp32 or bf16, got {Y.dtype}")
-    ws, size = 0, 0
-    if workspace is not None:
-        _same_device(d, workspace=workspace)
-        ws, size = workspace.data_ptr(), workspace.numel() * workspace.element_size()
-    else:
-        size = _w4_workspace(M, N, K, kind)
-        if size > 0:
-            workspace = torch.empty(size, dtype=torch.uint8, device=X.device)
-            ws = workspace.data_ptr()
     st = lib.bitnet_w4a16_matmul(X.data_ptr(), kind, packed.data_ptr(), scales.data_ptr(), M, N, K, K // groups,
-                                 Y.data_ptr(), y_kind, ws, size, FLAG_WEIGHTS_STATIC if weights_static else 0,
+                                 Y.data_ptr(), y_kind, FLAG_WEIGHTS_STATIC if weights_static else 0,
                                  _raw_stream(d))
     if st:
         _check(st, "bitnet_w4a16_matmul")

@@ -155,15 +155,9 @@ bitnet_status bitnet_quantize_weights_w4(const void *W, bitnet_dtype w_dtype, in
   return from_cuda(launch_quantize_weights_w4(W, w_dtype, N, K, group, packed, static_cast<uint16_t *>(scales), ctx));
 }
 
-size_t bitnet_w4a16_matmul_workspace_size(int64_t M, int64_t N, int64_t K, bitnet_dtype x_dtype) {
-  if (M <= 0 || N <= 0 || K <= 0 || M > kMaxCount || N > kMaxCount || K > kMaxK || !float_type(x_dtype)) return 0;
-  return w4_workspace(M, N, K, x_dtype);
-}
-
 bitnet_status bitnet_w4a16_matmul(const void *X, bitnet_dtype x_dtype, const uint8_t *packed,
                                   const void *scales, int64_t M, int64_t N, int64_t K, int32_t group, void *Y,
-                                  bitnet_dtype y_dtype, void *workspace, size_t workspace_bytes, uint32_t flags,
-                                  bitnet_stream_t stream) {
+                                  bitnet_dtype y_dtype, uint32_t flags, bitnet_stream_t stream) {
   if (!float_type(x_dtype) || !float_type(y_dtype) || (flags & ~BITNET_FLAG_WEIGHTS_STATIC) != 0)
     return BITNET_ERR_INVALID_ARG;
   if (M < 0 || N < 0 || M > kMaxCount || N > kMaxCount || K <= 0) return BITNET_ERR_INVALID_ARG;
@@ -176,15 +170,11 @@ bitnet_status bitnet_w4a16_matmul(const void *X, bitnet_dtype x_dtype, const uin
   if (overlap(X, static_cast<uint64_t>(M) * K * float_size(x_dtype), Y,
               static_cast<uint64_t>(M) * N * float_size(y_dtype)))
     return BITNET_ERR_INVALID_ARG;
-  const size_t need = w4_workspace(M, N, K, x_dtype);
-  if (need > 0) {
-    if (workspace == nullptr || workspace_bytes < need) return BITNET_ERR_WORKSPACE;
-    if (!aligned(workspace, 256)) return BITNET_ERR_MISALIGNED;
-  }
+  if (M > 8 * 65535) return BITNET_ERR_UNSUPPORTED_SHAPE;
   LaunchCtx ctx;
   if (const int st = launch_ctx_status(stream, &ctx)) return static_cast<bitnet_status>(st);
   return from_cuda(launch_w4(X, x_dtype, packed, static_cast<const uint16_t *>(scales), M, N, K, group, Y, y_dtype,
-                             workspace, (flags & BITNET_FLAG_WEIGHTS_STATIC) != 0, ctx));
+                             (flags & BITNET_FLAG_WEIGHTS_STATIC) != 0, ctx));
 }
 
 bitnet_status bitnet_token_logprobs(const void *logits, bitnet_dtype dtype, int64_t M, int64_t V, int64_t stride,

@@ -9,22 +9,25 @@
 // register.  Under the bf16 exponent of 128 a nibble is 128 + (c + 8), one
 // subtraction of 136 makes it c, exactly.
 //
-// The product is mma m16n8k16 with the weights as the A operand (16 output
+// The products are mma m16n8k16 with the weights as the A operand (16 output
 // features) and the tokens as the N axis.  The order of the K axis is free,
 // so a thread of a quad takes a quarter of the group: its words' halves are
 // its A fragments, and the 8 matching activations, 16 contiguous bytes of
 // the row, its B fragments.  Sums are fp32: inside a group by the tensor
-// core, over groups after the scale.  fp32 activations are split beforehand
-// into three bf16 terms that add up to 24 bits (a kernel of its own, into the
-// workspace), each with its own product into the same sums.
+// core, over groups after the scale.  fp32 activations are split into three
+// bf16 terms that add up to 24 bits, each with its own product into the same
+// sums.
+//   few tokens (up to 8, activations in shared memory whole): w4_few_kernel
+//   more: w4_many_kernel
+#include <atomic>
+
 #include "common.cuh"
 #include "internal.h"
 
 namespace bitnet {
 namespace {
 
-constexpr int kWarps = 8;
-constexpr int kRows = 16;  // features per CTA
+constexpr int kRows = 16;  // features of an MMA tile
 
 __device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                          uint32_t a3, uint32_t b0, uint32_t b1) {
@@ -35,9 +38,13 @@ __device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// Weights 2i and 2i + 1 of a word as two bf16.
+// Weights 2i and 2i + 1 of a word as two bf16, 136 too large.
+__device__ __forceinline__ uint32_t two_biased(uint32_t w, int i) {
+  return ((w >> (4 * i)) & 0x000F000Fu) | 0x43004300u;
+}
+// The same, exactly.
 __device__ __forceinline__ uint32_t two_codes(uint32_t w, int i) {
-  const uint32_t x = ((w >> (4 * i)) & 0x000F000Fu) | 0x43004300u, bias = 0x43084308u;  // 136, twice
+  const uint32_t x = two_biased(w, i), bias = 0x43084308u;  // 136, twice
   const __nv_bfloat162 v = __hsub2(*reinterpret_cast<const __nv_bfloat162 *>(&x),
                                    *reinterpret_cast<const __nv_bfloat162 *>(&bias));
   return *reinterpret_cast<const uint32_t *>(&v);
@@ -96,141 +103,447 @@ __global__ void __launch_bounds__(256) quantize_w4_kernel(const void *W, int64_t
   }
 }
 
-// fp32 activations as three bf16 terms, [3][M * K]: each term is the nearest
-// bf16 to what the ones before leave, so the three hold 24 bits.
-__global__ void __launch_bounds__(256) split_terms_kernel(const float *X, __nv_bfloat16 *out, int64_t n) {
-  pdl_wait();
-  pdl_launch_dependents();
-  for (int64_t i = 4 * (static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x); i < n;
-       i += 4 * static_cast<int64_t>(gridDim.x) * blockDim.x) {
-    const float4 v = *reinterpret_cast<const float4 *>(X + i);
-    float x[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int t = 0; t < 3; ++t) {
-      __nv_bfloat16 h[4];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        h[e] = __float2bfloat16_rn(x[e]);
-        const float left = __fsub_rn(x[e], __bfloat162float(h[e]));
-        // an infinity (or a value that rounds to one) is its first term alone
-        x[e] = isfinite(__bfloat162float(h[e])) ? left : 0.0f;
-      }
-      *reinterpret_cast<uint2 *>(out + t * n + i) = *reinterpret_cast<const uint2 *>(h);
-    }
-  }
-}
-
-// ------------------------------------------------------------ product
+// ------------------------------------------------------------ products
 struct W4Params {
-  const __nv_bfloat16 *x;  // [TERMS][M][K]
+  const void *x;           // [M][K] bf16 or fp32
   const uint8_t *packed;
   const uint16_t *scales;
   void *y;
   int64_t M, N, K;
+  int tiles;               // of output features
+  bool weights_static;
 };
 
-// A CTA: 16 features, 8 * NT tokens, every warp every 8th group.
-template <int G, int NT, int TERMS, int YK>
-__global__ void __launch_bounds__(kWarps * 32) w4_kernel(const W4Params p) {
-  constexpr int kWords = G / 32;  // words per thread, row and group
-  __shared__ float part[kWarps][kRows][8 * NT + 1];
+// 8 activations as they lie in memory, ...
+template <int TERMS> struct Raw {
+  uint4 v[TERMS == 1 ? 1 : 2];
+  __device__ __forceinline__ void load(const void *x, int64_t at) {
+    const uint4 *p = reinterpret_cast<const uint4 *>(static_cast<const uint8_t *>(x) + at * (TERMS == 1 ? 2 : 4));
+    v[0] = __ldg(p);
+    if (TERMS != 1) v[TERMS == 1 ? 0 : 1] = __ldg(p + 1);
+  }
+};
+// ... and as TERMS rows of bf16: themselves, or the nearest bf16 to what the
+// terms before leave of the fp32 value.
+template <int TERMS>
+__device__ __forceinline__ void split(const Raw<TERMS> &raw, uint4 (&out)[TERMS]) {
+  if (TERMS == 1) {
+    out[0] = raw.v[0];
+  } else {
+    const uint4 a = raw.v[0], b = raw.v[TERMS == 1 ? 0 : 1];
+    float v[8] = {__uint_as_float(a.x), __uint_as_float(a.y), __uint_as_float(a.z), __uint_as_float(a.w),
+                  __uint_as_float(b.x), __uint_as_float(b.y), __uint_as_float(b.z), __uint_as_float(b.w)};
+#pragma unroll
+    for (int t = 0; t < TERMS; ++t) {
+      uint32_t w[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * e], v[2 * e + 1]);
+        w[e] = *reinterpret_cast<const uint32_t *>(&h);
+        v[2 * e] = __fsub_rn(v[2 * e], __low2float(h));
+        v[2 * e + 1] = __fsub_rn(v[2 * e + 1], __high2float(h));
+      }
+      out[t] = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+  }
+}
+
+template <int YK> __device__ __forceinline__ void store_y(void *y, int64_t at, float v) {
+  if (YK == kF32)
+    static_cast<float *>(y)[at] = v;
+  else
+    static_cast<__nv_bfloat16 *>(y)[at] = __float2bfloat16_rn(v);
+}
+
+// A row's words of one group: thread t of a quad has a quarter.
+template <int G> struct Words {
+  static constexpr int kN = G / 32;
+  uint32_t w[kN];
+  __device__ __forceinline__ void load(const uint8_t *p) {
+    if (kN == 4) {
+      const uint4 v = __ldcs(reinterpret_cast<const uint4 *>(p));
+      w[0] = v.x; w[1 % kN] = v.y; w[2 % kN] = v.z; w[3 % kN] = v.w;
+    } else if (kN == 2) {
+      const uint2 v = __ldcs(reinterpret_cast<const uint2 *>(p));
+      w[0] = v.x; w[1 % kN] = v.y;
+    } else {
+      w[0] = __ldcs(reinterpret_cast<const uint32_t *>(p));
+    }
+  }
+};
+
+// Few tokens, bound by HBM.  A CTA of 4 warps goes over tiles of 16 features,
+// each warp over every 4th group, its weights and scales 4 groups ahead in
+// registers (across tiles); the warps' sums meet in shared memory, two
+// buffers, one barrier per tile.  The unpack is what the SM has to issue:
+// bf16 activations skip its subtraction (7 instructions per 8 weights instead
+// of 11) and take 136 times the group's activation sum away afterwards, an
+// fp32 error of 30 units of the group's sum at most.
+constexpr int kFewWarps = 4;
+constexpr int kAhead = 4;
+constexpr size_t kFewSmem = 72 * 1024;
+inline int64_t few_pitch(int64_t K) { return K + 8; }  // activations per row in shared memory
+inline size_t few_smem(int64_t M, int64_t K, int group, int terms) {
+  return static_cast<size_t>(terms) * (M + 1) * few_pitch(K) * 2 + (terms == 1 ? 8 * static_cast<size_t>(K / group) * 4 : 0);
+}
+
+template <int G, int TERMS, int YK>
+__global__ void __launch_bounds__(kFewWarps * 32) w4_few_kernel(const W4Params p) {
+  constexpr int kWords = G / 32;
+  extern __shared__ __align__(16) uint8_t smem[];
+  __shared__ float part[2][kFewWarps][kRows][9];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  const int K = static_cast<int>(p.K), groups = K / G, M = static_cast<int>(p.M), pitch = K + 8;
+  __nv_bfloat16 *xs = reinterpret_cast<__nv_bfloat16 *>(smem);                       // [TERMS][M + 1][pitch], the last row 0
+  float *xsum = reinterpret_cast<float *>(smem + static_cast<size_t>(TERMS) * (M + 1) * pitch * 2);  // [8][groups]
+
+  // the warp's groups, in order: group q of tile `tile`
+  Words<G> wa[kAhead], wb[kAhead];
+  uint16_t sa[kAhead], sb[kAhead];
+  int tile_in = blockIdx.x, q_in = warp;  // the next group to load, and where it lies
+  if (q_in >= groups) tile_in = p.tiles;
+  const uint8_t *pa, *pb;
+  const uint16_t *qa, *qb;
+  auto enter = [&]() {
+    const int64_t n0 = static_cast<int64_t>(tile_in) * kRows + g;
+    // (rows past the end read the last one and are not stored)
+    const int64_t na = n0 < p.N ? n0 : p.N - 1, nb = n0 + 8 < p.N ? n0 + 8 : p.N - 1;
+    pa = p.packed + na * (K / 2) + warp * (G / 2) + t * (G / 8);
+    pb = p.packed + nb * (K / 2) + warp * (G / 2) + t * (G / 8);
+    qa = p.scales + na * groups + warp;
+    qb = p.scales + nb * groups + warp;
+  };
+  enter();
+  auto fetch = [&](int slot) {
+    if (tile_in >= p.tiles) return;
+    wa[slot].load(pa);
+    wb[slot].load(pb);
+    sa[slot] = __ldg(qa);
+    sb[slot] = __ldg(qb);
+    pa += kFewWarps * (G / 2);
+    pb += kFewWarps * (G / 2);
+    qa += kFewWarps;
+    qb += kFewWarps;
+    q_in += kFewWarps;
+    if (q_in >= groups) {
+      q_in = warp;
+      tile_in += gridDim.x;
+      enter();
+    }
+  };
+  if (p.weights_static) {
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) fetch(i);
+  }
   pdl_wait();
   pdl_launch_dependents();
+  if (!p.weights_static) {
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) fetch(i);
+  }
+  for (int i = threadIdx.x; i < TERMS * (K / 8); i += kFewWarps * 32) {
+    const int k = i / (K / 8), c = i - k * (K / 8);
+    *reinterpret_cast<uint4 *>(xs + static_cast<size_t>(k * (M + 1) + M) * pitch + c * 8) = make_uint4(0, 0, 0, 0);
+  }
+  for (int i = threadIdx.x; i < M * (K / 8); i += kFewWarps * 32) {
+    const int m = i / (K / 8), c = i - m * (K / 8);
+    Raw<TERMS> raw;
+    raw.load(p.x, static_cast<int64_t>(m) * K + c * 8);
+    uint4 v[TERMS];
+    split<TERMS>(raw, v);
+#pragma unroll
+    for (int k = 0; k < TERMS; ++k)
+      *reinterpret_cast<uint4 *>(xs + static_cast<size_t>(k * (M + 1) + m) * pitch + c * 8) = v[k];
+  }
+  if (TERMS == 1) {
+    __syncthreads();
+    for (int i = threadIdx.x; i < 8 * groups; i += kFewWarps * 32) {
+      const int m = i / groups, q = i - m * groups;
+      float s = 0.0f;
+      if (m < M) {
+        const uint4 *src = reinterpret_cast<const uint4 *>(xs + static_cast<size_t>(m) * pitch + q * G);
+#pragma unroll 4
+        for (int e = 0; e < G / 8; ++e) {
+          const uint4 v = src[e];
+          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+          for (int z = 0; z < 4; ++z) s += __uint_as_float(w[z] << 16) + __uint_as_float(w[z] & 0xFFFF0000u);
+        }
+      }
+      xsum[i] = -136.0f * s;
+    }
+  }
+  __syncthreads();
+
+  const __nv_bfloat16 *x_lane = xs + static_cast<size_t>(g < M ? g : M) * pitch + t * (G / 4);
+  int tile = blockIdx.x, q = warp, buffer = 0;
+  float y[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+  while (tile < p.tiles) {
+#pragma unroll
+    for (int slot = 0; slot < kAhead; ++slot) {
+      if (q < groups) {
+        float c[2][4];  // two chains of sums
+#pragma unroll
+        for (int e = 0; e < 4; ++e) c[0][e] = c[1][e] = 0.0f;
+        if (TERMS == 1) {
+          c[0][0] = c[0][2] = xsum[(2 * t) * groups + q];
+          c[0][1] = c[0][3] = xsum[(2 * t + 1) * groups + q];
+        }
+#pragma unroll
+        for (int i = 0; i < kWords; ++i) {
+          uint32_t fa[4], fb[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            fa[e] = TERMS == 1 ? two_biased(wa[slot].w[i], e) : two_codes(wa[slot].w[i], e);
+            fb[e] = TERMS == 1 ? two_biased(wb[slot].w[i], e) : two_codes(wb[slot].w[i], e);
+          }
+#pragma unroll
+          for (int k = TERMS - 1; k >= 0; --k) {
+            const uint4 x = *reinterpret_cast<const uint4 *>(x_lane + static_cast<size_t>(k) * (M + 1) * pitch + q * G + i * 8);
+            mma_bf16(c[0], fa[0], fb[0], fa[1], fb[1], x.x, x.y);
+            mma_bf16(c[1], fa[2], fb[2], fa[3], fb[3], x.z, x.w);
+          }
+        }
+        const float s0 = bf16_value(sa[slot]), s1 = bf16_value(sb[slot]);
+        y[0] = __fmaf_rn(s0, c[0][0] + c[1][0], y[0]);
+        y[1] = __fmaf_rn(s0, c[0][1] + c[1][1], y[1]);
+        y[2] = __fmaf_rn(s1, c[0][2] + c[1][2], y[2]);
+        y[3] = __fmaf_rn(s1, c[0][3] + c[1][3], y[3]);
+        fetch(slot);
+        q += kFewWarps;
+      }
+      if (q >= groups) {  // the warp's last group of the tile
+        float (&mine)[kRows][9] = part[buffer][warp];
+        mine[g][2 * t] = y[0];
+        mine[g][2 * t + 1] = y[1];
+        mine[g + 8][2 * t] = y[2];
+        mine[g + 8][2 * t + 1] = y[3];
+        __syncthreads();
+        const int row = threadIdx.x % kRows, col = threadIdx.x / kRows;
+        const int64_t n = static_cast<int64_t>(tile) * kRows + row;
+        if (n < p.N && col < M) {
+          float v = 0.0f;
+#pragma unroll
+          for (int w = 0; w < kFewWarps; ++w) v += part[buffer][w][row][col];
+          store_y<YK>(p.y, col * p.N + n, v);
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) y[e] = 0.0f;
+        q = warp;
+        buffer ^= 1;
+        tile += gridDim.x;
+        if (tile >= p.tiles) break;
+      }
+    }
+  }
+}
+
+// More tokens.  A CTA of 8 warps takes 128 features (a warp 16) and 8 * NT
+// tokens over a slice of K, in chunks of 128 weights: the chunk's activations
+// (terms) in shared memory, two buffers, the next ones and the next weights on
+// their way in registers.  The CTAs of a cluster take the slices of K and add
+// their sums up through distributed shared memory, in slice order.
+constexpr int kManyWarps = 8;
+constexpr int kManyRows = kManyWarps * kRows;
+constexpr int kChunkK = 128, kChunkPitch = kChunkK + 8;
+template <int NT, int TERMS> constexpr size_t many_smem() {
+  return 2 * static_cast<size_t>(TERMS) * 8 * NT * kChunkPitch * 2 > sizeof(float) * kManyRows * (8 * NT + 1)
+             ? 2 * static_cast<size_t>(TERMS) * 8 * NT * kChunkPitch * 2
+             : sizeof(float) * kManyRows * (8 * NT + 1);
+}
+
+template <int G, int NT, int TERMS, int YK>
+__global__ void __launch_bounds__(kManyWarps * 32, 2) w4_many_kernel(const W4Params p) {
+  constexpr int kWords = G / 32, kGroups = kChunkK / G;
+  constexpr int kUnits = 8 * NT * (kChunkK / 8);                       // 8 activations each
+  constexpr int kPer = (kUnits + kManyWarps * 32 - 1) / (kManyWarps * 32);
+  extern __shared__ __align__(16) uint8_t smem[];
+  __nv_bfloat16 *xs = reinterpret_cast<__nv_bfloat16 *>(smem);         // [2][TERMS][8 NT][pitch]
+  constexpr int kBuffer = TERMS * 8 * NT * kChunkPitch;
+  float *part = reinterpret_cast<float *>(smem);                       // [128][8 NT + 1], afterwards
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  const int64_t n0 = static_cast<int64_t>(blockIdx.x) * kRows;
+  uint32_t slices;
+  asm("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(slices));
+  const uint32_t slice = cluster_ctarank();
+  const int64_t n0 = static_cast<int64_t>(blockIdx.x / slices) * kManyRows + warp * kRows;
   const int64_t m0 = static_cast<int64_t>(blockIdx.y) * 8 * NT;
-  const int groups = static_cast<int>(p.K / G);
+  const int64_t K = p.K, groups = K / G;
+  const int64_t chunks = (K + kChunkK - 1) / kChunkK;
+  const int64_t c0 = chunks * slice / slices, c1 = chunks * (slice + 1) / slices;
   // rows and tokens past the end read the last one and are not stored
   const int64_t na = n0 + g < p.N ? n0 + g : p.N - 1, nb = n0 + g + 8 < p.N ? n0 + g + 8 : p.N - 1;
-  const uint8_t *wa = p.packed + na * (p.K / 2) + t * (G / 8), *wb = p.packed + nb * (p.K / 2) + t * (G / 8);
-  const __nv_bfloat16 *xr[NT];
+
+  Words<G> wa[kGroups], wb[kGroups];
+  uint16_t sa[kGroups], sb[kGroups];
+  Raw<TERMS> xr[kPer];
+  Words<G> wa1[kGroups], wb1[kGroups];  // the next chunk's
+  uint16_t sa1[kGroups], sb1[kGroups];
+  auto fetch_weights = [&](int64_t c) {
 #pragma unroll
-  for (int j = 0; j < NT; ++j) {
-    const int64_t m = m0 + 8 * j + g < p.M ? m0 + 8 * j + g : p.M - 1;
-    xr[j] = p.x + m * p.K + t * (G / 4);
-  }
+    for (int q = 0; q < kGroups; ++q) {
+      const int64_t at = c * kGroups + q;
+      if (c < c1 && at < groups) {
+        wa1[q].load(p.packed + na * (K / 2) + at * (G / 2) + t * (G / 8));
+        wb1[q].load(p.packed + nb * (K / 2) + at * (G / 2) + t * (G / 8));
+        sa1[q] = __ldg(p.scales + na * groups + at);
+        sb1[q] = __ldg(p.scales + nb * groups + at);
+      }
+    }
+  };
+  auto fetch_x = [&](int64_t c) {
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const int u = threadIdx.x + i * kManyWarps * 32;
+      const int64_t k = c * kChunkK + u % (kChunkK / 8) * 8;
+      if (u < kUnits && c < c1 && k < K) {
+        const int64_t m = m0 + u / (kChunkK / 8) < p.M ? m0 + u / (kChunkK / 8) : p.M - 1;
+        xr[i].load(p.x, m * K + k);
+      }
+    }
+  };
+  auto keep_x = [&](int buffer) {
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const int u = threadIdx.x + i * kManyWarps * 32;
+      if (u < kUnits) {
+        uint4 v[TERMS];
+        split<TERMS>(xr[i], v);
+#pragma unroll
+        for (int k = 0; k < TERMS; ++k)
+          *reinterpret_cast<uint4 *>(xs + buffer * kBuffer + (k * 8 * NT + u / (kChunkK / 8)) * kChunkPitch +
+                                     u % (kChunkK / 8) * 8) = v[k];
+      }
+    }
+  };
+  if (p.weights_static) fetch_weights(c0);
+  pdl_wait();
+  pdl_launch_dependents();
+  if (!p.weights_static) fetch_weights(c0);
+  fetch_x(c0);
   float y[NT][4];
 #pragma unroll
   for (int j = 0; j < NT; ++j)
 #pragma unroll
     for (int e = 0; e < 4; ++e) y[j][e] = 0.0f;
-  for (int q = warp; q < groups; q += kWarps) {
-    uint32_t a[kWords], b[kWords];
+  for (int64_t c = c0; c < c1; ++c) {
+    const int buffer = static_cast<int>(c & 1);
 #pragma unroll
-    for (int i = 0; i < kWords; ++i) {
-      a[i] = __ldg(reinterpret_cast<const uint32_t *>(wa + static_cast<int64_t>(q) * (G / 2)) + i);
-      b[i] = __ldg(reinterpret_cast<const uint32_t *>(wb + static_cast<int64_t>(q) * (G / 2)) + i);
+    for (int q = 0; q < kGroups; ++q) {
+      wa[q] = wa1[q];
+      wb[q] = wb1[q];
+      sa[q] = sa1[q];
+      sb[q] = sb1[q];
     }
-    const float sa = bf16_value(__ldg(p.scales + na * groups + q)), sb = bf16_value(__ldg(p.scales + nb * groups + q));
-    float c[NT][4];
+    keep_x(buffer);  // (last read two chunks ago, before the last barrier)
+    fetch_weights(c + 1);
+    fetch_x(c + 1);
+    __syncthreads();
 #pragma unroll
-    for (int j = 0; j < NT; ++j)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) c[j][e] = 0.0f;
-#pragma unroll
-    for (int i = 0; i < kWords; ++i) {
-      uint32_t fa[4], fb[4];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        fa[e] = two_codes(a[i], e);
-        fb[e] = two_codes(b[i], e);
-      }
+    for (int q = 0; q < kGroups; ++q) {
+      if (c * kGroups + q >= groups) break;
+      float acc[NT][4];
 #pragma unroll
       for (int j = 0; j < NT; ++j)
 #pragma unroll
-        for (int k = TERMS - 1; k >= 0; --k) {
-          const uint4 x = __ldg(reinterpret_cast<const uint4 *>(xr[j] + k * p.M * p.K + static_cast<int64_t>(q) * G) + i);
-          mma_bf16(c[j], fa[0], fb[0], fa[1], fb[1], x.x, x.y);
-          mma_bf16(c[j], fa[2], fb[2], fa[3], fb[3], x.z, x.w);
-        }
-    }
+        for (int e = 0; e < 4; ++e) acc[j][e] = 0.0f;
 #pragma unroll
-    for (int j = 0; j < NT; ++j) {
-      y[j][0] = __fmaf_rn(sa, c[j][0], y[j][0]);
-      y[j][1] = __fmaf_rn(sa, c[j][1], y[j][1]);
-      y[j][2] = __fmaf_rn(sb, c[j][2], y[j][2]);
-      y[j][3] = __fmaf_rn(sb, c[j][3], y[j][3]);
+      for (int i = 0; i < kWords; ++i) {
+        uint32_t fa[4], fb[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          fa[e] = two_codes(wa[q].w[i], e);
+          fb[e] = two_codes(wb[q].w[i], e);
+        }
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+          for (int k = TERMS - 1; k >= 0; --k) {
+            const uint4 x = *reinterpret_cast<const uint4 *>(xs + buffer * kBuffer + (k * 8 * NT + 8 * j + g) * kChunkPitch +
+                                                             q * G + t * (G / 4) + i * 8);
+            mma_bf16(acc[j], fa[0], fb[0], fa[1], fb[1], x.x, x.y);
+            mma_bf16(acc[j], fa[2], fb[2], fa[3], fb[3], x.z, x.w);
+          }
+      }
+      const float s0 = bf16_value(sa[q]), s1 = bf16_value(sb[q]);
+#pragma unroll
+      for (int j = 0; j < NT; ++j) {
+        y[j][0] = __fmaf_rn(s0, acc[j][0], y[j][0]);
+        y[j][1] = __fmaf_rn(s0, acc[j][1], y[j][1]);
+        y[j][2] = __fmaf_rn(s1, acc[j][2], y[j][2]);
+        y[j][3] = __fmaf_rn(s1, acc[j][3], y[j][3]);
+      }
     }
   }
+  __syncthreads();  // the activations are done with
+  constexpr int kPitch = 8 * NT + 1;
 #pragma unroll
   for (int j = 0; j < NT; ++j) {
-    part[warp][g][8 * j + 2 * t] = y[j][0];
-    part[warp][g][8 * j + 2 * t + 1] = y[j][1];
-    part[warp][g + 8][8 * j + 2 * t] = y[j][2];
-    part[warp][g + 8][8 * j + 2 * t + 1] = y[j][3];
+    float *at = part + (warp * kRows + g) * kPitch + 8 * j + 2 * t;
+    at[0] = y[j][0];
+    at[1] = y[j][1];
+    at[8 * kPitch] = y[j][2];
+    at[8 * kPitch + 1] = y[j][3];
   }
-  __syncthreads();
-  for (int i = threadIdx.x; i < kRows * 8 * NT; i += kWarps * 32) {
-    const int row = i % kRows, col = i / kRows;
-    if (n0 + row >= p.N || m0 + col >= p.M) continue;
+  if (slices > 1)
+    cluster_sync();
+  else
+    __syncthreads();
+  // each CTA adds up and stores its share of the rows
+  const int rows = kManyRows / static_cast<int>(slices);
+  const int64_t first = static_cast<int64_t>(blockIdx.x / slices) * kManyRows + slice * rows;
+  for (int i = threadIdx.x; i < rows * 8 * NT; i += kManyWarps * 32) {
+    const int row = i % rows, col = i / rows;
+    if (first + row >= p.N || m0 + col >= p.M) continue;
+    const float *at = part + (slice * rows + row) * kPitch + col;
     float v = 0.0f;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) v = __fadd_rn(v, part[w][row][col]);
-    const int64_t o = (m0 + col) * p.N + n0 + row;
-    if (YK == kF32)
-      static_cast<float *>(p.y)[o] = v;
-    else
-      static_cast<__nv_bfloat16 *>(p.y)[o] = __float2bfloat16_rn(v);
+    for (uint32_t s = 0; s < slices; ++s) {
+      float x;
+      asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(x) : "r"(mapa_shared(at, s)) : "memory");
+      v += x;
+    }
+    store_y<YK>(p.y, (m0 + col) * p.N + first + row, v);
   }
+  if (slices > 1) cluster_sync();  // the others have read this CTA's sums
 }
 
-template <int G, int NT, int TERMS>
-cudaError_t launch_y(const W4Params &p, int y_kind, const LaunchCtx &ctx) {
-  const dim3 grid(static_cast<unsigned>(ceil_div(p.N, kRows)), static_cast<unsigned>(ceil_div(p.M, 8 * NT)));
-  return y_kind == kF32 ? launch_k(w4_kernel<G, NT, TERMS, kF32>, grid, dim3(kWarps * 32), 0, ctx, p)
-                        : launch_k(w4_kernel<G, NT, TERMS, kBF16>, grid, dim3(kWarps * 32), 0, ctx, p);
+template <int G, int TERMS, int YK>
+cudaError_t launch_few(W4Params p, const LaunchCtx &ctx) {
+  const size_t smem = few_smem(p.M, p.K, G, TERMS);
+  static std::atomic<uint64_t> ready;
+  if (const cudaError_t e = allow_smem(w4_few_kernel<G, TERMS, YK>, kFewSmem, ready, ctx)) return e;
+  p.tiles = static_cast<int>(ceil_div(p.N, kRows));
+  // resident CTAs only: each goes on to further tiles with its pipeline full
+  int per_sm = static_cast<int>(size_t(200 * 1024) / (smem + 8 * 1024));
+  per_sm = per_sm > 5 ? 5 : (per_sm < 1 ? 1 : per_sm);
+  const int most = ctx.num_sms * per_sm;
+  const dim3 grid(static_cast<unsigned>(p.tiles < most ? p.tiles : most));
+  return launch_k(w4_few_kernel<G, TERMS, YK>, grid, dim3(kFewWarps * 32), smem, ctx, p);
 }
-template <int G, int TERMS>
-cudaError_t launch_nt(const W4Params &p, int y_kind, const LaunchCtx &ctx) {
-  if (p.M <= 8) return launch_y<G, 1, TERMS>(p, y_kind, ctx);
-  if (p.M <= 16) return launch_y<G, 2, TERMS>(p, y_kind, ctx);
-  return launch_y<G, 4, TERMS>(p, y_kind, ctx);
+template <int G, int NT, int TERMS, int YK>
+cudaError_t launch_many(W4Params p, const LaunchCtx &ctx) {
+  constexpr size_t smem = many_smem<NT, TERMS>();
+  static std::atomic<uint64_t> ready;
+  if (const cudaError_t e = allow_smem(w4_many_kernel<G, NT, TERMS, YK>, smem, ready, ctx)) return e;
+  p.tiles = static_cast<int>(ceil_div(p.N, kManyRows));
+  const int64_t blocks = p.tiles * ceil_div(p.M, 8 * NT), chunks = ceil_div(p.K, kChunkK);
+  unsigned slices = 1;  // of K, until the CTAs fill the GPU
+  while (slices < 8 && blocks * slices * 2 <= 2 * ctx.num_sms && slices * 2 <= chunks) slices *= 2;
+  const dim3 grid(static_cast<unsigned>(p.tiles) * slices, static_cast<unsigned>(ceil_div(p.M, 8 * NT)));
+  return launch_k_cluster(w4_many_kernel<G, NT, TERMS, YK>, grid, dim3(kManyWarps * 32), smem, slices, ctx, p);
 }
-template <int TERMS>
-cudaError_t launch_g(const W4Params &p, int group, int y_kind, const LaunchCtx &ctx) {
-  if (group == 128) return launch_nt<128, TERMS>(p, y_kind, ctx);
-  if (group == 64) return launch_nt<64, TERMS>(p, y_kind, ctx);
-  return launch_nt<32, TERMS>(p, y_kind, ctx);
+template <int G, int TERMS, int YK>
+cudaError_t launch_m(const W4Params &p, const LaunchCtx &ctx) {
+  if (p.M <= 8 && few_smem(p.M, p.K, G, TERMS) <= kFewSmem) return launch_few<G, TERMS, YK>(p, ctx);
+  if (p.M <= 8) return launch_many<G, 1, TERMS, YK>(p, ctx);
+  if (p.M <= 16) return launch_many<G, 2, TERMS, YK>(p, ctx);
+  if (p.M <= 24) return launch_many<G, 3, TERMS, YK>(p, ctx);
+  return launch_many<G, 4, TERMS, YK>(p, ctx);
+}
+template <int TERMS, int YK>
+cudaError_t launch_g(const W4Params &p, int group, const LaunchCtx &ctx) {
+  if (group == 128) return launch_m<128, TERMS, YK>(p, ctx);
+  if (group == 64) return launch_m<64, TERMS, YK>(p, ctx);
+  return launch_m<32, TERMS, YK>(p, ctx);
 }
 
 template <int KIND, int G>
@@ -257,25 +570,13 @@ cudaError_t launch_quantize_weights_w4(const void *W, int w_kind, int64_t N, int
                         : quantize_g<kBF16>(W, words, group, packed, scales, ctx);
 }
 
-size_t w4_workspace(int64_t M, int64_t N, int64_t K, int x_kind) {
-  (void)N;
-  return x_kind == kF32 ? (static_cast<size_t>(M) * K * 6 + 255) & ~size_t(255) : 0;
-}
-
 cudaError_t launch_w4(const void *X, int x_kind, const uint8_t *packed, const uint16_t *scales,
                       int64_t M, int64_t N, int64_t K, int group, void *Y, int y_kind,
-                      void *workspace, bool weights_static, const LaunchCtx &ctx) {
-  (void)weights_static;
-  W4Params p = {static_cast<const __nv_bfloat16 *>(X), packed, scales, Y, M, N, K};
-  if (x_kind != kF32) return launch_g<1>(p, group, y_kind, ctx);
-  int64_t blocks = ceil_div(M * K, 1024);
-  if (blocks > ctx.num_sms * 8) blocks = ctx.num_sms * 8;
-  __nv_bfloat16 *terms = static_cast<__nv_bfloat16 *>(workspace);
-  const cudaError_t e = launch_k(split_terms_kernel, dim3(static_cast<unsigned>(blocks)), dim3(256), 0, ctx,
-                                 static_cast<const float *>(X), terms, M * K);
-  if (e != cudaSuccess) return e;
-  p.x = terms;
-  return launch_g<3>(p, group, y_kind, ctx);
+                      bool weights_static, const LaunchCtx &ctx) {
+  const W4Params p = {X, packed, scales, Y, M, N, K, 0, weights_static};
+  if (x_kind == kF32)
+    return y_kind == kF32 ? launch_g<3, kF32>(p, group, ctx) : launch_g<3, kBF16>(p, group, ctx);
+  return y_kind == kF32 ? launch_g<1, kF32>(p, group, ctx) : launch_g<1, kBF16>(p, group, ctx);
 }
 
 }  // namespace bitnet

@@ -198,10 +198,9 @@ cudaError_t launch_kv_attention_prompt(const KvCache &cache, const KvBatch &batc
 // gemv_w4.cu: 4-bit weights [N][K / 2] with bf16 scales [N][K / group].
 cudaError_t launch_quantize_weights_w4(const void *W, int w_kind, int64_t N, int64_t K, int group,
                                        uint8_t *packed, uint16_t *scales, const LaunchCtx &ctx);
-size_t w4_workspace(int64_t M, int64_t N, int64_t K, int x_kind);
 cudaError_t launch_w4(const void *X, int x_kind, const uint8_t *packed, const uint16_t *scales,
                       int64_t M, int64_t N, int64_t K, int group, void *Y, int y_kind,
-                      void *workspace, bool weights_static, const LaunchCtx &ctx);
+                      bool weights_static, const LaunchCtx &ctx);
 
 // token_logprobs.cu
 constexpr int kLogprobsMaxTop = 32;
