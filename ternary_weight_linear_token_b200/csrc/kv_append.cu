@@ -72,10 +72,12 @@ __global__ void __launch_bounds__(kMaxThreads) kv_append_kernel(const AppendPara
   pdl_wait();
   pdl_launch_dependents();
   const int P = p.cache.page_tokens, D = p.cache.head_dim, H = p.cache.heads;
-  const int64_t b = blockIdx.x / p.tiles;
+  const int page_shift = 31 - __clz(P), row_shift = 28 - __clz(D);  // D / 8 chunks per row
+  const int b = blockIdx.x / static_cast<unsigned>(p.tiles);
   const int which = blockIdx.y & 1, h = blockIdx.y >> 1;
-  const int64_t len = p.batch.lens[b];
-  int64_t r0 = b, r1 = b + 1;
+  // (positions and rows fit 32 bits)
+  const int len = p.batch.lens[b];
+  int r0 = b, r1 = b + 1;
   if (p.batch.offsets != nullptr) {
     r0 = p.batch.offsets[b];
     r1 = p.batch.offsets[b + 1];
@@ -86,25 +88,26 @@ __global__ void __launch_bounds__(kMaxThreads) kv_append_kernel(const AppendPara
     return;  // rows, or positions, that do not exist: nothing of the sequence is written
   }
   if (r1 == r0) return;
-  const int64_t first = len - (r1 - r0);  // position of row r0
+  const int first = len - (r1 - r0);  // position of row r0
   int8_t *codes = which ? p.cache.v_codes : p.cache.k_codes;
   float *scales = which ? p.cache.v_scales : p.cache.k_scales;
   const void *x = p.x[which];
   const int64_t stride = p.stride[which];
-  const int row_chunks = D / 8;
+  const int *table = p.batch.pages + static_cast<int64_t>(b) * p.batch.max_pages;
 
-  for (int64_t i = first / P + blockIdx.x % p.tiles; i <= (len - 1) / P; i += p.tiles) {
-    const int64_t page = p.batch.pages[b * p.batch.max_pages + i];
+  for (int i = (first >> page_shift) + static_cast<int>(blockIdx.x - b * static_cast<unsigned>(p.tiles)); i <= (len - 1) >> page_shift;
+       i += p.tiles) {
+    const int64_t page = table[i];
     if (page < 0 || page >= p.cache.pages) {
       if (threadIdx.x == 0) record_status(p.status, kStatusRange);
       continue;
     }
-    const int64_t lo = first > i * P ? first : i * P;             // the page's new positions
-    const int64_t hi = len < (i + 1) * P ? len : (i + 1) * P;
-    const int older = static_cast<int>(lo - i * P);
-    const int chunks = static_cast<int>(hi - lo) * row_chunks;
+    const int lo = first > i * P ? first : i * P;             // the page's new positions
+    const int hi = len - i * P < P ? len : (i + 1) * P;
+    const int older = lo - i * P;
+    const int chunks = (hi - lo) << row_shift;
     const float was = older > 0 ? scales[page * H + h] : 0.0f;
-    const int64_t base = (r0 + (lo - first)) * stride + static_cast<int64_t>(h) * D;
+    const int64_t base = static_cast<int64_t>(r0 + (lo - first)) * stride + h * D;
     int8_t *out = codes + ((page * H + h) * P + older) * D;
 
     float v[kMaxChunks][8];
@@ -113,7 +116,7 @@ __global__ void __launch_bounds__(kMaxThreads) kv_append_kernel(const AppendPara
     for (int j = 0; j < kMaxChunks; ++j) {
       const int c = threadIdx.x + j * blockDim.x;
       if (c < chunks) {
-        load8<KIND>(x, base + static_cast<int64_t>(c / row_chunks) * stride + c % row_chunks * 8, v[j]);
+        load8<KIND>(x, base + (c >> row_shift) * stride + ((c << 3) & (D - 1)), v[j]);
 #pragma unroll
         for (int e = 0; e < 8; ++e) peak = fmaxf(peak, fabsf(v[j][e]));
       }
@@ -122,7 +125,7 @@ __global__ void __launch_bounds__(kMaxThreads) kv_append_kernel(const AppendPara
     // told of fewer new tokens): the rest is read twice
     for (int c = threadIdx.x + kMaxChunks * blockDim.x; c < chunks; c += blockDim.x) {
       float w[8];
-      load8<KIND>(x, base + static_cast<int64_t>(c / row_chunks) * stride + c % row_chunks * 8, w);
+      load8<KIND>(x, base + (c >> row_shift) * stride + ((c << 3) & (D - 1)), w);
 #pragma unroll
       for (int e = 0; e < 8; ++e) peak = fmaxf(peak, fabsf(w[e]));
     }
@@ -133,7 +136,7 @@ __global__ void __launch_bounds__(kMaxThreads) kv_append_kernel(const AppendPara
     if (older > 0 && d > was) {
       const float f = __fmul_rn(was, r);
       uint32_t *w = reinterpret_cast<uint32_t *>(codes + (page * H + h) * P * D);
-      const int skip = static_cast<int>(hi - lo) * D / 4;  // the new rows
+      const int skip = (hi - lo) * D / 4;  // the new rows
       for (int i = threadIdx.x; i < P * D / 4 - skip; i += blockDim.x) {
         const int c = i < older * D / 4 ? i : i + skip;
         const uint32_t u = w[c];
@@ -158,7 +161,7 @@ __global__ void __launch_bounds__(kMaxThreads) kv_append_kernel(const AppendPara
     }
     for (int c = threadIdx.x + kMaxChunks * blockDim.x; c < chunks; c += blockDim.x) {
       float w[8];
-      load8<KIND>(x, base + static_cast<int64_t>(c / row_chunks) * stride + c % row_chunks * 8, w);
+      load8<KIND>(x, base + (c >> row_shift) * stride + ((c << 3) & (D - 1)), w);
       store(c, w);
     }
     if (threadIdx.x == 0) scales[page * H + h] = d;

@@ -21,6 +21,7 @@
 // Bound by HBM for many rows (one read of the logits), by latency for one.
 #include "common.cuh"
 #include "internal.h"
+#include "pairs.cuh"
 
 namespace bitnet {
 namespace {
@@ -55,6 +56,16 @@ __device__ __forceinline__ float below(float x, float m) {
   asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(__fsub_rn(x, m)), "f"(-1e30f));
   return y;
 }
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+__device__ __forceinline__ float min3(float a, float b, float c) {
+  float r;
+  asm("min.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
 // The sums of two parts, at the larger maximum.
 __device__ __forceinline__ Sums join(const Sums &a, const Sums &b) {
   const float m = fmaxf(a.m, b.m);
@@ -74,6 +85,17 @@ __device__ __forceinline__ Sums join(const Sums &a, const Sums &b) {
     }
   }
   return r;
+}
+
+// The sums of all lanes, in every lane.
+__device__ __forceinline__ Sums join_lanes(Sums w, int lane) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    const Sums b = {__shfl_xor_sync(0xffffffffu, w.m, o), __shfl_xor_sync(0xffffffffu, w.s, o),
+                    __shfl_xor_sync(0xffffffffu, w.u, o)};
+    w = (lane & o) != 0 ? join(b, w) : join(w, b);  // both lanes the same way round
+  }
+  return w;
 }
 
 __device__ __forceinline__ uint64_t key_of(float x, uint32_t index) {
@@ -181,9 +203,12 @@ __global__ void __launch_bounds__(kThreads, 2) token_logprobs_kernel(const Logpr
   Sums a = {-INFINITY, 0.0f, 0.0f};
   int64_t best_chunk = c0 + threadIdx.x;
   auto add = [&](const float (&v)[N], int64_t c) {
-    float cm = v[0];
+    float cm = fmaxf(v[0], v[1]), cl = fminf(v[0], v[1]);
 #pragma unroll
-    for (int e = 1; e < N; ++e) cm = fmaxf(cm, v[e]);
+    for (int e = 2; e < N; e += 2) {
+      cm = max3(cm, v[e], v[e + 1]);
+      cl = min3(cl, v[e], v[e + 1]);
+    }
     if (cm > a.m) {
       best_chunk = c;
       if (a.m != -INFINITY) {
@@ -199,12 +224,31 @@ __global__ void __launch_bounds__(kThreads, 2) token_logprobs_kernel(const Logpr
         if (v[e] != v[e]) a.s = v[e];
       return;
     }
+    if (cl == -INFINITY) {  // d e^d of -infinity is 0: with a lower limit
 #pragma unroll
-    for (int e = 0; e < N; ++e) {
-      const float d = below(v[e], a.m), x = ex2(__fmul_rn(d, kLog2e));
-      a.s += x;
-      a.u = __fmaf_rn(x, d, a.u);
+      for (int e = 0; e < N; ++e) {
+        const float d = below(v[e], a.m), x = ex2(__fmul_rn(d, kLog2e));
+        a.s += x;
+        a.u = __fmaf_rn(x, d, a.u);
+      }
+      return;
     }
+    const uint64_t minus_m = pair(-a.m, -a.m), log2e = pair(kLog2e, kLog2e);
+    uint64_t s = pair(0.0f, 0.0f), u = s;
+#pragma unroll
+    for (int e = 0; e < N; e += 2) {
+      const uint64_t d = add2(pair(v[e], v[e + 1]), minus_m);
+      float t0, t1;
+      unpair(mul2(d, log2e), t0, t1);
+      const uint64_t x = pair(ex2(t0), ex2(t1));
+      s = add2(s, x);
+      u = fma2(x, d, u);
+    }
+    float s0, s1;
+    unpair(s, s0, s1);
+    a.s += s0 + s1;
+    unpair(u, s0, s1);
+    a.u += s0 + s1;
   };
   int64_t c = c0 + threadIdx.x;
   for (; c + 3 * kThreads < c1; c += 4 * kThreads) {
@@ -220,13 +264,15 @@ __global__ void __launch_bounds__(kThreads, 2) token_logprobs_kernel(const Logpr
     add(v, c);
   }
   Sums w = a;
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    const Sums b = {__shfl_xor_sync(0xffffffffu, w.m, o), __shfl_xor_sync(0xffffffffu, w.s, o),
-                    __shfl_xor_sync(0xffffffffu, w.u, o)};
-    w = (lane & o) != 0 ? join(b, w) : join(w, b);  // both lanes the same way round
-  }
+  w = join_lanes(w, lane);
   if (lane == 0) sums[warp] = w;
+  __syncthreads();
+  if (warp == 0) {  // the CTA's
+    w = lane < kWarps ? sums[lane] : Sums{-INFINITY, 0.0f, 0.0f};
+    w = join_lanes(w, lane);
+    __syncwarp();
+    if (lane == 0) sums[0] = w;
+  }
 
   // ---- top k of this CTA's part
   uint64_t mine = 0;
@@ -277,22 +323,18 @@ __global__ void __launch_bounds__(kThreads, 2) token_logprobs_kernel(const Logpr
     return;
   }
   if (warp == 0) {
-    Sums all = sums[0];
-    for (int i = 1; i < kWarps; ++i) all = join(all, sums[i]);
-    for (uint32_t r = 1; r < ctas; ++r) {
-      const uint32_t at = mapa_shared(sums, r);
-      Sums part = {-INFINITY, 0.0f, 0.0f};
-      for (int i = 0; i < kWarps; ++i) {
-        Sums b;
-        asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(b.m) : "r"(at + i * 12));
-        asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(b.s) : "r"(at + i * 12 + 4));
-        asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(b.u) : "r"(at + i * 12 + 8));
-        part = join(part, b);
-      }
-      all = join(all, part);
-      if (p.top > 0) {
+    Sums all = {-INFINITY, 0.0f, 0.0f};
+    if (lane < static_cast<int>(ctas)) {
+      const uint32_t at = mapa_shared(sums, static_cast<uint32_t>(lane));
+      asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(all.m) : "r"(at) : "memory");
+      asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(all.s) : "r"(at + 4) : "memory");
+      asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(all.u) : "r"(at + 8) : "memory");
+    }
+    all = join_lanes(all, lane);
+    if (p.top > 0) {
+      for (uint32_t r = 1; r < ctas; ++r) {
         uint64_t b;
-        asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(b) : "r"(mapa_shared(list, r) + lane * 8));
+        asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(b) : "r"(mapa_shared(list, r) + lane * 8) : "memory");
         mine = merge32(mine, b, lane);
       }
     }
