@@ -20,6 +20,17 @@ capturable in a CUDA graph (``capture``):
     ``bitnet_decode_chain``, one kernel for the whole stack, with the
     normalisation folded into the next layer's QKV projection.
 Both fill the same buffers (``outs``), so every link can be checked.
+
+The per-launch form can also run what stands around the projections:
+  * ``caches``, a ``KVCache`` per layer: attention over the tokens that have
+    run takes the place of the stand-in.  The fused QKV output holds the query
+    heads (the first d columns), then the key heads, then the value heads; the
+    token's keys and values are appended to the layer's cache and its queries
+    attend to it (no position encoding: the caller's, if any, belongs into the
+    weights or between the calls).
+  * ``head`` [vocabulary, d]: the output head, kept in 4 bits with a scale per
+    128 weights; ``run`` leaves the token's logits in ``logits`` (fp32) and
+    ``score`` gives log probabilities, entropy and top alternatives of them.
 """
 
 from __future__ import annotations
@@ -27,19 +38,27 @@ from __future__ import annotations
 import torch
 
 from . import (bitnet_decode_chain, bitnet_decode_chain_steps, bitnet_decode_chain_workspace_size,
-               bitnet_quantize_weights, bitnet_rms_norm, bitnet_rms_norm_w158a8_matmul,
-               bitnet_w158a8_matmul)
+               bitnet_kv_append, bitnet_kv_attention, bitnet_kv_attention_workspace_size,
+               bitnet_quantize_weights, bitnet_quantize_weights_w4, bitnet_rms_norm,
+               bitnet_rms_norm_w158a8_matmul, bitnet_token_logprobs, bitnet_w158a8_matmul,
+               bitnet_w4a16_matmul)
 
 
 class DecodeChain:
     def __init__(self, weights, device="cuda:0", weights_static: bool = True,
-                 persistent: bool = False, quantized=None):
+                 persistent: bool = False, quantized=None, caches=None,
+                 head: torch.Tensor | None = None):
         """weights: list over layers of a list of 4 (W [N, K] float tensor,
         relu2) pairs in the order qkv, o, up, down (any iterable: a
         generator keeps only one layer's latent weights alive at a time).
         Weights are quantised on the device once, here.
         quantized: instead of weights, the ``layers`` of another DecodeChain
-        (packed weights shared, nothing quantised again)."""
+        (packed weights shared, nothing quantised again).
+        caches: a KVCache per layer (per-launch form only): one sequence, whose
+        token p lies in page p // page_tokens of each; ``lens`` counts its
+        tokens, ``reset`` starts over, and a token past the last page is
+        refused on the device (bitnet_get_device_status).
+        head: the output head's weights [vocabulary, d], fp32 or bf16."""
         self.device = torch.device(device)
         self.weights_static = weights_static
         if quantized is not None:
@@ -66,6 +85,15 @@ class DecodeChain:
             self.outs.append(bufs)
         self.graph = None
         self.persistent = persistent
+        self.caches = None
+        if caches is not None:
+            self._take_caches(list(caches))
+        self.head = None
+        if head is not None:
+            if head.dim() != 2 or head.shape[1] != d:
+                raise ValueError(f"head must be [vocabulary, {d}]")
+            self.head = bitnet_quantize_weights_w4(head.to(self.device).contiguous(), group=128)
+            self.logits = torch.empty((1, head.shape[0]), dtype=torch.float32, device=self.device)
         if persistent:
             steps = []
             for li, (proj, bufs) in enumerate(zip(self.layers, self.outs)):
@@ -78,6 +106,51 @@ class DecodeChain:
             self._keep = steps
             self.workspace = torch.zeros(bitnet_decode_chain_workspace_size(self._steps),
                                          dtype=torch.uint8, device=self.device)
+
+    def _take_caches(self, caches):
+        if self.persistent:
+            raise ValueError("the persistent chain runs projections only: caches need the per-launch form")
+        if len(caches) != len(self.layers):
+            raise ValueError(f"{len(caches)} caches for {len(self.layers)} layers")
+        first = caches[0]
+        shape = (first.num_pages, first.heads, first.page_tokens, first.head_dim)
+        heads, rest = divmod(self.d, first.head_dim)
+        for li, (c, proj) in enumerate(zip(caches, self.layers)):
+            if (c.num_pages, c.heads, c.page_tokens, c.head_dim) != shape:
+                raise ValueError("the layers' caches must have the same shape")
+            if rest or heads % c.heads or proj[0]["N"] != (heads + 2 * c.heads) * c.head_dim:
+                raise ValueError(f"layer {li}: {proj[0]['N']} QKV columns are not {self.d} of queries and "
+                                 f"2 x {c.heads} heads of {c.head_dim}")
+        self.caches, self.q_heads = caches, heads
+        self.pages = torch.arange(first.num_pages, dtype=torch.int32, device=self.device)[None]
+        self.lens = torch.zeros(1, dtype=torch.int32, device=self.device)
+        # attention output of each layer, kept like the other links
+        self.attended = [torch.empty((1, heads, first.head_dim), dtype=torch.bfloat16, device=self.device)
+                         for _ in caches]
+        size = bitnet_kv_attention_workspace_size(first, torch.bfloat16, 1, heads, 1, first.num_pages)
+        self._kv_workspace = torch.empty(max(size, 1), dtype=torch.uint8, device=self.device)
+        self._kv_launches = 3 if size > 0 else 2
+
+    def reset(self) -> None:
+        """Starts a new sequence: the next token is its first."""
+        if self.caches is not None:
+            self.lens.zero_()
+
+    def _attend(self, li: int, qkv: torch.Tensor) -> torch.Tensor:
+        """The token's keys and values into layer li's cache, its queries over it."""
+        c = self.caches[li]
+        q, k, v = qkv.view(1, -1, c.head_dim).split((self.q_heads, c.heads, c.heads), dim=1)
+        bitnet_kv_append(c, k, v, self.pages, self.lens)
+        out = self.attended[li]
+        bitnet_kv_attention(c, q, self.pages, self.lens, O=out, workspace=self._kv_workspace)
+        return out.view(1, self.d)
+
+    def score(self, tokens: torch.Tensor, top: int = 0):
+        """(logprob, entropy, top_ids, top_logprobs) of the last token's logits
+        (bitnet_token_logprobs); tokens [1] int64."""
+        if self.head is None:
+            raise ValueError("the chain has no head")
+        return bitnet_token_logprobs(self.logits, tokens, top=top)
 
     @property
     def packed_bytes(self) -> int:
@@ -92,7 +165,9 @@ class DecodeChain:
             self.x_in.copy_(x0)
         if self.persistent:
             bitnet_decode_chain(self._steps, self.x_in, self.workspace, y_norm=self.outs[-1][4])
-            return self.outs[-1][4]
+            return self._finish()
+        if self.caches is not None:
+            self.lens.add_(1)
         for li, (proj, bufs) in enumerate(zip(self.layers, self.outs)):
             qkv, o, up, down = proj
             if li == 0:
@@ -102,20 +177,33 @@ class DecodeChain:
                 bitnet_rms_norm_w158a8_matmul(prev[3], qkv["packed"], qkv["gamma"],
                                               X_normed=prev[4], relu2=qkv["relu2"], Y=bufs[0],
                                               weights_static=self.weights_static)
-            q = bufs[0][:, : self.d]          # contiguous for one token
+            if self.caches is not None:
+                q = self._attend(li, bufs[0])
+            else:
+                q = bufs[0][:, : self.d]      # contiguous for one token
             self._bl(q, o, bufs[1])
             self._bl(bufs[1], up, bufs[2])
             self._bl(bufs[2], down, bufs[3])
         last = self.outs[-1]
         bitnet_rms_norm(last[3], Y=last[4])
-        return last[4]
+        return self._finish()
+
+    def _finish(self) -> torch.Tensor:
+        x = self.outs[-1][4]
+        if self.head is not None:
+            bitnet_w4a16_matmul(x, *self.head, Y=self.logits, weights_static=self.weights_static)
+        return x
 
     def capture(self) -> torch.cuda.CUDAGraph:
-        """Capture one token through the whole stack in a CUDA graph."""
+        """Capture one token through the whole stack in a CUDA graph.  (With
+        caches the warm-up writes the next token's place, which the next run
+        writes again.)"""
         s = torch.cuda.Stream(self.device)
         s.wait_stream(torch.cuda.current_stream(self.device))
         with torch.cuda.stream(s):
             self.run()  # warm-up outside capture
+            if self.caches is not None:
+                self.lens.sub_(1)
         torch.cuda.current_stream(self.device).wait_stream(s)
         g = torch.cuda.CUDAGraph()
         with torch.cuda.graph(g):
@@ -124,4 +212,7 @@ class DecodeChain:
         return g
 
     def launches_per_token(self) -> int:
-        return 1 if self.persistent else 4 * len(self.layers) + 1
+        head = 0 if self.head is None else 1
+        if self.persistent:
+            return 1 + head
+        return (4 + (0 if self.caches is None else self._kv_launches)) * len(self.layers) + 1 + head

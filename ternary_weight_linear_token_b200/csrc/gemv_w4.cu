@@ -112,6 +112,7 @@ struct W4Params {
   int64_t M, N, K;
   int tiles;               // of output features
   bool weights_static;
+  int *status;
 };
 
 // 8 activations as they lie in memory, ...
@@ -161,89 +162,85 @@ template <int G> struct Words {
   uint32_t w[kN];
   __device__ __forceinline__ void load(const uint8_t *p) {
     if (kN == 4) {
-      const uint4 v = __ldcs(reinterpret_cast<const uint4 *>(p));
+      const uint4 v = *reinterpret_cast<const uint4 *>(p);
       w[0] = v.x; w[1 % kN] = v.y; w[2 % kN] = v.z; w[3 % kN] = v.w;
     } else if (kN == 2) {
-      const uint2 v = __ldcs(reinterpret_cast<const uint2 *>(p));
+      const uint2 v = *reinterpret_cast<const uint2 *>(p);
       w[0] = v.x; w[1 % kN] = v.y;
     } else {
-      w[0] = __ldcs(reinterpret_cast<const uint32_t *>(p));
+      w[0] = *reinterpret_cast<const uint32_t *>(p);
     }
   }
 };
 
-// Few tokens, bound by HBM.  A CTA of 4 warps goes over tiles of 16 features,
-// each warp over every 4th group, its weights and scales 4 groups ahead in
-// registers (across tiles); the warps' sums meet in shared memory, two
-// buffers, one barrier per tile.  The unpack is what the SM has to issue:
-// bf16 activations skip its subtraction (7 instructions per 8 weights instead
-// of 11) and take 136 times the group's activation sum away afterwards, an
-// fp32 error of 30 units of the group's sum at most.
-constexpr int kFewWarps = 4;
-constexpr int kAhead = 4;
-constexpr size_t kFewSmem = 72 * 1024;
-inline int64_t few_pitch(int64_t K) { return K + 8; }  // activations per row in shared memory
-inline size_t few_smem(int64_t M, int64_t K, int group, int terms) {
-  return static_cast<size_t>(terms) * (M + 1) * few_pitch(K) * 2 + (terms == 1 ? 8 * static_cast<size_t>(K / group) * 4 : 0);
+// Few tokens, bound by HBM.  A tile of 16 features is contiguous in memory,
+// and so are its scales: a CTA of 4 warps goes over tiles whose bulk copies
+// are a tile ahead in shared memory (two stages: a third costs a CTA per SM
+// and time, 55 against 49 us for 128256 x 2560), each warp over every 4th
+// group; the warps' sums meet in shared memory, one barrier per tile, which
+// also hands the stage back.  The unpack is what the SM has to issue: bf16
+// activations skip its subtraction (7 instructions per 8 weights instead of
+// 11) and take 136 times the group's activation sum away afterwards, an fp32
+// error of 30 units of the group's sum at most.
+constexpr int kFewWarps = 4, kFewStages = 2;
+constexpr size_t kFewSmem = 112 * 1024;  // of a CTA, two per SM
+struct FewPlan {
+  int x_bytes, w_bytes, stage_bytes, stages;
+  size_t smem;
+};
+// false: the tiles are too long
+inline bool few_plan(int64_t M, int64_t K, int group, int terms, FewPlan *f) {
+  const int64_t groups = K / group;
+  const int64_t x = terms * (M + 1) * (K + 8) * 2 + (terms == 1 ? 8 * groups * 4 : 0), w = 8 * K, s = 32 * groups;
+  const int64_t x16 = (x + 15) / 16 * 16, stage = w + s;
+  if (x16 + kFewStages * stage + 64 > static_cast<int64_t>(kFewSmem)) return false;
+  f->x_bytes = static_cast<int>(x16);
+  f->w_bytes = static_cast<int>(w);
+  f->stage_bytes = static_cast<int>(stage);
+  f->stages = kFewStages;
+  f->smem = static_cast<size_t>(x16 + kFewStages * stage + 64);
+  return true;
 }
 
 template <int G, int TERMS, int YK>
-__global__ void __launch_bounds__(kFewWarps * 32) w4_few_kernel(const W4Params p) {
+__global__ void __launch_bounds__(kFewWarps * 32) w4_few_kernel(const W4Params p, const FewPlan f) {
   constexpr int kWords = G / 32;
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ float part[2][kFewWarps][kRows][9];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int K = static_cast<int>(p.K), groups = K / G, M = static_cast<int>(p.M), pitch = K + 8;
-  __nv_bfloat16 *xs = reinterpret_cast<__nv_bfloat16 *>(smem);                       // [TERMS][M + 1][pitch], the last row 0
-  float *xsum = reinterpret_cast<float *>(smem + static_cast<size_t>(TERMS) * (M + 1) * pitch * 2);  // [8][groups]
-
-  // the warp's groups, in order: group q of tile `tile`
-  Words<G> wa[kAhead], wb[kAhead];
-  uint16_t sa[kAhead], sb[kAhead];
-  int tile_in = blockIdx.x, q_in = warp;  // the next group to load, and where it lies
-  if (q_in >= groups) tile_in = p.tiles;
-  const uint8_t *pa, *pb;
-  const uint16_t *qa, *qb;
-  auto enter = [&]() {
-    const int64_t n0 = static_cast<int64_t>(tile_in) * kRows + g;
-    // (rows past the end read the last one and are not stored)
-    const int64_t na = n0 < p.N ? n0 : p.N - 1, nb = n0 + 8 < p.N ? n0 + 8 : p.N - 1;
-    pa = p.packed + na * (K / 2) + warp * (G / 2) + t * (G / 8);
-    pb = p.packed + nb * (K / 2) + warp * (G / 2) + t * (G / 8);
-    qa = p.scales + na * groups + warp;
-    qb = p.scales + nb * groups + warp;
+  __nv_bfloat16 *xs = reinterpret_cast<__nv_bfloat16 *>(smem);       // [TERMS][M + 1][pitch], the last row 0
+  float *xsum = reinterpret_cast<float *>(smem + TERMS * (M + 1) * pitch * 2);  // [8][groups]
+  uint8_t *ring = smem + f.x_bytes;
+  uint64_t *full = reinterpret_cast<uint64_t *>(ring + f.stages * f.stage_bytes);
+  if (threadIdx.x < f.stages) mbar_init(&full[threadIdx.x], 1);
+  fence_barrier_init();
+  __syncthreads();
+  // (thread 0) the tile's rows and scales; the last tile's may be fewer, and
+  // then the scales' bytes no multiple of 16: everybody reads those itself
+  auto copy = [&](int tile, int stage) {
+    const int64_t n0 = static_cast<int64_t>(tile) * kRows;
+    const int rows = p.N - n0 < kRows ? static_cast<int>(p.N - n0) : kRows;
+    uint8_t *to = ring + stage * f.stage_bytes;
+    const uint32_t w = rows * (K / 2), s = rows == kRows ? 32 * groups : 0;
+    mbar_arrive_expect_tx(&full[stage], w + s);
+    bulk_g2s(to, p.packed + n0 * (K / 2), w, &full[stage]);
+    if (s > 0) bulk_g2s(to + f.w_bytes, p.scales + n0 * groups, s, &full[stage]);
   };
-  enter();
-  auto fetch = [&](int slot) {
-    if (tile_in >= p.tiles) return;
-    wa[slot].load(pa);
-    wb[slot].load(pb);
-    sa[slot] = __ldg(qa);
-    sb[slot] = __ldg(qb);
-    pa += kFewWarps * (G / 2);
-    pb += kFewWarps * (G / 2);
-    qa += kFewWarps;
-    qb += kFewWarps;
-    q_in += kFewWarps;
-    if (q_in >= groups) {
-      q_in = warp;
-      tile_in += gridDim.x;
-      enter();
-    }
+  auto start = [&]() {
+    if (threadIdx.x == 0)
+      for (int i = 0; i < f.stages; ++i) {
+        const int64_t tile = blockIdx.x + static_cast<int64_t>(i) * gridDim.x;
+        if (tile < p.tiles) copy(static_cast<int>(tile), i);
+      }
   };
-  if (p.weights_static) {
-#pragma unroll
-    for (int i = 0; i < kAhead; ++i) fetch(i);
-  }
+  if (p.weights_static) start();
   pdl_wait();
   pdl_launch_dependents();
-  if (!p.weights_static) {
-#pragma unroll
-    for (int i = 0; i < kAhead; ++i) fetch(i);
-  }
+  if (!p.weights_static) start();
   for (int i = threadIdx.x; i < TERMS * (K / 8); i += kFewWarps * 32) {
     const int k = i / (K / 8), c = i - k * (K / 8);
-    *reinterpret_cast<uint4 *>(xs + static_cast<size_t>(k * (M + 1) + M) * pitch + c * 8) = make_uint4(0, 0, 0, 0);
+    *reinterpret_cast<uint4 *>(xs + (k * (M + 1) + M) * pitch + c * 8) = make_uint4(0, 0, 0, 0);
   }
   for (int i = threadIdx.x; i < M * (K / 8); i += kFewWarps * 32) {
     const int m = i / (K / 8), c = i - m * (K / 8);
@@ -252,8 +249,7 @@ __global__ void __launch_bounds__(kFewWarps * 32) w4_few_kernel(const W4Params p
     uint4 v[TERMS];
     split<TERMS>(raw, v);
 #pragma unroll
-    for (int k = 0; k < TERMS; ++k)
-      *reinterpret_cast<uint4 *>(xs + static_cast<size_t>(k * (M + 1) + m) * pitch + c * 8) = v[k];
+    for (int k = 0; k < TERMS; ++k) *reinterpret_cast<uint4 *>(xs + (k * (M + 1) + m) * pitch + c * 8) = v[k];
   }
   if (TERMS == 1) {
     __syncthreads();
@@ -261,7 +257,7 @@ __global__ void __launch_bounds__(kFewWarps * 32) w4_few_kernel(const W4Params p
       const int m = i / groups, q = i - m * groups;
       float s = 0.0f;
       if (m < M) {
-        const uint4 *src = reinterpret_cast<const uint4 *>(xs + static_cast<size_t>(m) * pitch + q * G);
+        const uint4 *src = reinterpret_cast<const uint4 *>(xs + m * pitch + q * G);
 #pragma unroll 4
         for (int e = 0; e < G / 8; ++e) {
           const uint4 v = src[e];
@@ -275,65 +271,74 @@ __global__ void __launch_bounds__(kFewWarps * 32) w4_few_kernel(const W4Params p
   }
   __syncthreads();
 
-  const __nv_bfloat16 *x_lane = xs + static_cast<size_t>(g < M ? g : M) * pitch + t * (G / 4);
-  int tile = blockIdx.x, q = warp, buffer = 0;
-  float y[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-  while (tile < p.tiles) {
+  const __nv_bfloat16 *x_lane = xs + (g < M ? g : M) * pitch + t * (G / 4);
+  int stage = 0, buffer = 0;
+  uint32_t phase = 0;
+  for (int tile = blockIdx.x; tile < p.tiles; tile += gridDim.x) {
+    const bool ok = mbar_wait(&full[stage], phase, nullptr);  // (recorded below)
+    if (!ok && threadIdx.x == 0) record_status(p.status, kStatusTimeout);
+    const uint8_t *w = ring + stage * f.stage_bytes + g * (K / 2) + t * (G / 8);
+    const uint16_t *s = reinterpret_cast<const uint16_t *>(ring + stage * f.stage_bytes + f.w_bytes) + g * groups;
+    int s8 = 8 * groups;  // to the scales of row g + 8
+    if (p.N - static_cast<int64_t>(tile) * kRows < kRows) {
+      const int64_t na = static_cast<int64_t>(tile) * kRows + g;
+      s = p.scales + (na < p.N ? na : p.N - 1) * groups;
+      s8 = static_cast<int>((na + 8 < p.N ? na + 8 : p.N - 1) - (na < p.N ? na : p.N - 1)) * groups;
+    }
+    float y[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 4
+    for (int q = warp; q < groups; q += kFewWarps) {
+      Words<G> wa, wb;
+      wa.load(w + q * (G / 2));
+      wb.load(w + q * (G / 2) + 4 * K);
+      float c[2][4];  // two chains of sums
 #pragma unroll
-    for (int slot = 0; slot < kAhead; ++slot) {
-      if (q < groups) {
-        float c[2][4];  // two chains of sums
-#pragma unroll
-        for (int e = 0; e < 4; ++e) c[0][e] = c[1][e] = 0.0f;
-        if (TERMS == 1) {
-          c[0][0] = c[0][2] = xsum[(2 * t) * groups + q];
-          c[0][1] = c[0][3] = xsum[(2 * t + 1) * groups + q];
-        }
-#pragma unroll
-        for (int i = 0; i < kWords; ++i) {
-          uint32_t fa[4], fb[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            fa[e] = TERMS == 1 ? two_biased(wa[slot].w[i], e) : two_codes(wa[slot].w[i], e);
-            fb[e] = TERMS == 1 ? two_biased(wb[slot].w[i], e) : two_codes(wb[slot].w[i], e);
-          }
-#pragma unroll
-          for (int k = TERMS - 1; k >= 0; --k) {
-            const uint4 x = *reinterpret_cast<const uint4 *>(x_lane + static_cast<size_t>(k) * (M + 1) * pitch + q * G + i * 8);
-            mma_bf16(c[0], fa[0], fb[0], fa[1], fb[1], x.x, x.y);
-            mma_bf16(c[1], fa[2], fb[2], fa[3], fb[3], x.z, x.w);
-          }
-        }
-        const float s0 = bf16_value(sa[slot]), s1 = bf16_value(sb[slot]);
-        y[0] = __fmaf_rn(s0, c[0][0] + c[1][0], y[0]);
-        y[1] = __fmaf_rn(s0, c[0][1] + c[1][1], y[1]);
-        y[2] = __fmaf_rn(s1, c[0][2] + c[1][2], y[2]);
-        y[3] = __fmaf_rn(s1, c[0][3] + c[1][3], y[3]);
-        fetch(slot);
-        q += kFewWarps;
+      for (int e = 0; e < 4; ++e) c[0][e] = c[1][e] = 0.0f;
+      if (TERMS == 1) {
+        c[0][0] = c[0][2] = xsum[(2 * t) * groups + q];
+        c[0][1] = c[0][3] = xsum[(2 * t + 1) * groups + q];
       }
-      if (q >= groups) {  // the warp's last group of the tile
-        float (&mine)[kRows][9] = part[buffer][warp];
-        mine[g][2 * t] = y[0];
-        mine[g][2 * t + 1] = y[1];
-        mine[g + 8][2 * t] = y[2];
-        mine[g + 8][2 * t + 1] = y[3];
-        __syncthreads();
-        const int row = threadIdx.x % kRows, col = threadIdx.x / kRows;
-        const int64_t n = static_cast<int64_t>(tile) * kRows + row;
-        if (n < p.N && col < M) {
-          float v = 0.0f;
 #pragma unroll
-          for (int w = 0; w < kFewWarps; ++w) v += part[buffer][w][row][col];
-          store_y<YK>(p.y, col * p.N + n, v);
+      for (int i = 0; i < kWords; ++i) {
+        uint32_t fa[4], fb[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          fa[e] = TERMS == 1 ? two_biased(wa.w[i], e) : two_codes(wa.w[i], e);
+          fb[e] = TERMS == 1 ? two_biased(wb.w[i], e) : two_codes(wb.w[i], e);
         }
 #pragma unroll
-        for (int e = 0; e < 4; ++e) y[e] = 0.0f;
-        q = warp;
-        buffer ^= 1;
-        tile += gridDim.x;
-        if (tile >= p.tiles) break;
+        for (int k = TERMS - 1; k >= 0; --k) {
+          const uint4 x = *reinterpret_cast<const uint4 *>(x_lane + k * (M + 1) * pitch + q * G + i * 8);
+          mma_bf16(c[0], fa[0], fb[0], fa[1], fb[1], x.x, x.y);
+          mma_bf16(c[1], fa[2], fb[2], fa[3], fb[3], x.z, x.w);
+        }
       }
+      const float s0 = bf16_value(s[q]), s1 = bf16_value(s[q + s8]);
+      y[0] = __fmaf_rn(s0, c[0][0] + c[1][0], y[0]);
+      y[1] = __fmaf_rn(s0, c[0][1] + c[1][1], y[1]);
+      y[2] = __fmaf_rn(s1, c[0][2] + c[1][2], y[2]);
+      y[3] = __fmaf_rn(s1, c[0][3] + c[1][3], y[3]);
+    }
+    float (&mine)[kRows][9] = part[buffer][warp];
+    mine[g][2 * t] = y[0];
+    mine[g][2 * t + 1] = y[1];
+    mine[g + 8][2 * t] = y[2];
+    mine[g + 8][2 * t + 1] = y[3];
+    if (__syncthreads_or(!ok)) return;  // (nothing that gave up is stored)
+    if (threadIdx.x == 0 && tile + static_cast<int64_t>(f.stages) * gridDim.x < p.tiles)
+      copy(tile + f.stages * static_cast<int>(gridDim.x), stage);
+    const int row = threadIdx.x % kRows, col = threadIdx.x / kRows;
+    const int64_t n = static_cast<int64_t>(tile) * kRows + row;
+    if (n < p.N && col < M) {
+      float v = 0.0f;
+#pragma unroll
+      for (int e = 0; e < kFewWarps; ++e) v += part[buffer][e][row][col];
+      store_y<YK>(p.y, col * p.N + n, v);
+    }
+    buffer ^= 1;
+    if (++stage == f.stages) {
+      stage = 0;
+      phase ^= 1u;
     }
   }
 }
@@ -507,17 +512,16 @@ __global__ void __launch_bounds__(kManyWarps * 32, 2) w4_many_kernel(const W4Par
 }
 
 template <int G, int TERMS, int YK>
-cudaError_t launch_few(W4Params p, const LaunchCtx &ctx) {
-  const size_t smem = few_smem(p.M, p.K, G, TERMS);
+cudaError_t launch_few(W4Params p, const FewPlan &f, const LaunchCtx &ctx) {
   static std::atomic<uint64_t> ready;
   if (const cudaError_t e = allow_smem(w4_few_kernel<G, TERMS, YK>, kFewSmem, ready, ctx)) return e;
   p.tiles = static_cast<int>(ceil_div(p.N, kRows));
-  // resident CTAs only: each goes on to further tiles with its pipeline full
-  int per_sm = static_cast<int>(size_t(200 * 1024) / (smem + 8 * 1024));
+  // resident CTAs only: each goes on to further tiles with its copies ahead
+  int per_sm = static_cast<int>(size_t(224 * 1024) / (f.smem + 6 * 1024));
   per_sm = per_sm > 5 ? 5 : (per_sm < 1 ? 1 : per_sm);
   const int most = ctx.num_sms * per_sm;
   const dim3 grid(static_cast<unsigned>(p.tiles < most ? p.tiles : most));
-  return launch_k(w4_few_kernel<G, TERMS, YK>, grid, dim3(kFewWarps * 32), smem, ctx, p);
+  return launch_k(w4_few_kernel<G, TERMS, YK>, grid, dim3(kFewWarps * 32), f.smem, ctx, p, f);
 }
 template <int G, int NT, int TERMS, int YK>
 cudaError_t launch_many(W4Params p, const LaunchCtx &ctx) {
@@ -533,7 +537,8 @@ cudaError_t launch_many(W4Params p, const LaunchCtx &ctx) {
 }
 template <int G, int TERMS, int YK>
 cudaError_t launch_m(const W4Params &p, const LaunchCtx &ctx) {
-  if (p.M <= 8 && few_smem(p.M, p.K, G, TERMS) <= kFewSmem) return launch_few<G, TERMS, YK>(p, ctx);
+  FewPlan f;
+  if (p.M <= 8 && few_plan(p.M, p.K, G, TERMS, &f)) return launch_few<G, TERMS, YK>(p, f, ctx);
   if (p.M <= 8) return launch_many<G, 1, TERMS, YK>(p, ctx);
   if (p.M <= 16) return launch_many<G, 2, TERMS, YK>(p, ctx);
   if (p.M <= 24) return launch_many<G, 3, TERMS, YK>(p, ctx);
@@ -573,7 +578,7 @@ cudaError_t launch_quantize_weights_w4(const void *W, int w_kind, int64_t N, int
 cudaError_t launch_w4(const void *X, int x_kind, const uint8_t *packed, const uint16_t *scales,
                       int64_t M, int64_t N, int64_t K, int group, void *Y, int y_kind,
                       bool weights_static, const LaunchCtx &ctx) {
-  const W4Params p = {X, packed, scales, Y, M, N, K, 0, weights_static};
+  const W4Params p = {X, packed, scales, Y, M, N, K, 0, weights_static, ctx.status};
   if (x_kind == kF32)
     return y_kind == kF32 ? launch_g<3, kF32>(p, group, ctx) : launch_g<3, kBF16>(p, group, ctx);
   return y_kind == kF32 ? launch_g<1, kF32>(p, group, ctx) : launch_g<1, kBF16>(p, group, ctx);

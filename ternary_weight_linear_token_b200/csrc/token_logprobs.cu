@@ -50,10 +50,11 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-// x - m, at least -1e30 (e^d is 0 there, and so is d e^d); NaN stays NaN.
+// x - m, at least -1e28 (e^d is 0 there, and so is d e^d, times any sum); NaN
+// stays NaN.
 __device__ __forceinline__ float below(float x, float m) {
   float y;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(__fsub_rn(x, m)), "f"(-1e30f));
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(__fsub_rn(x, m)), "f"(-1e28f));
   return y;
 }
 __device__ __forceinline__ float max3(float a, float b, float c) {
@@ -66,34 +67,23 @@ __device__ __forceinline__ float min3(float a, float b, float c) {
   asm("min.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
 }
-// The sums of two parts, at the larger maximum.
+// The sums of two parts, at the larger maximum; the same whichever comes
+// first.  (Equal maxima, infinite ones too, count as they are; a part without
+// a maximum has s = 0, or NaN, which goes on.)
 __device__ __forceinline__ Sums join(const Sums &a, const Sums &b) {
   const float m = fmaxf(a.m, b.m);
-  Sums r = {m, 0.0f, 0.0f};
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const Sums &c = i ? b : a;
-    if (c.m == m) {  // also the infinities
-      r.s += c.s;
-      r.u += c.u;
-    } else if (c.m == -INFINITY) {  // nothing, or only NaN
-      r.s += c.s;
-    } else {
-      const float d = below(c.m, m), f = ex2(d * kLog2e);
-      r.s = __fmaf_rn(f, c.s, r.s);
-      r.u = __fmaf_rn(f, __fmaf_rn(d, c.s, c.u), r.u);
-    }
-  }
-  return r;
+  const float da = a.m == m ? 0.0f : below(a.m, m), db = b.m == m ? 0.0f : below(b.m, m);
+  const float fa = ex2(__fmul_rn(da, kLog2e)), fb = ex2(__fmul_rn(db, kLog2e));
+  return {m, __fadd_rn(__fmul_rn(fa, a.s), __fmul_rn(fb, b.s)),
+          __fadd_rn(__fmul_rn(fa, __fmaf_rn(da, a.s, a.u)), __fmul_rn(fb, __fmaf_rn(db, b.s, b.u)))};
 }
-
 // The sums of all lanes, in every lane.
-__device__ __forceinline__ Sums join_lanes(Sums w, int lane) {
+__device__ __forceinline__ Sums join_lanes(Sums w) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
     const Sums b = {__shfl_xor_sync(0xffffffffu, w.m, o), __shfl_xor_sync(0xffffffffu, w.s, o),
                     __shfl_xor_sync(0xffffffffu, w.u, o)};
-    w = (lane & o) != 0 ? join(b, w) : join(w, b);  // both lanes the same way round
+    w = join(w, b);
   }
   return w;
 }
@@ -149,6 +139,20 @@ __device__ __forceinline__ uint64_t block_best(uint64_t a, uint64_t *list, int w
 template <int KIND> struct Vec {
   static constexpr int kN = KIND == kF32 ? 4 : 8;
 };
+// The values of 16 bytes.
+template <int KIND>
+__device__ __forceinline__ void values_of(const uint4 &u, float *v) {
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    if (KIND == kF32) {
+      v[e] = __uint_as_float(w[e]);
+    } else {
+      v[2 * e] = __uint_as_float(w[e] << 16);
+      v[2 * e + 1] = __uint_as_float(w[e] & 0xFFFF0000u);
+    }
+  }
+}
 // Chunk c of the row: elements c * kN - skew + e, those outside [0, V) as
 // -infinity.
 template <int KIND>
@@ -157,18 +161,7 @@ __device__ __forceinline__ void load_chunk(const void *row, int64_t c, int skew,
   constexpr int N = Vec<KIND>::kN;
   const int64_t i0 = c * N - skew;
   if (i0 >= 0 && i0 + N <= V) {
-    if (KIND == kF32) {
-      const float4 f = __ldg(reinterpret_cast<const float4 *>(static_cast<const float *>(row) + i0));
-      v[0] = f.x; v[1] = f.y; v[2] = f.z; v[3] = f.w;
-    } else {
-      const uint4 u = __ldg(reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(row) + i0));
-      const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        v[2 * e] = __uint_as_float(w[e] << 16);
-        v[2 * e + 1 < N ? 2 * e + 1 : 0] = __uint_as_float(w[e] & 0xFFFF0000u);
-      }
-    }
+    values_of<KIND>(__ldg(reinterpret_cast<const uint4 *>(static_cast<const char *>(row) + i0 * (16 / N))), v);
   } else {
 #pragma unroll
     for (int e = 0; e < N; ++e) {
@@ -181,7 +174,7 @@ __device__ __forceinline__ void load_chunk(const void *row, int64_t c, int skew,
 }
 
 template <int KIND>
-__global__ void __launch_bounds__(kThreads, 2) token_logprobs_kernel(const LogprobParams p) {
+__global__ void __launch_bounds__(kThreads, 3) token_logprobs_kernel(const LogprobParams p) {
   constexpr int N = Vec<KIND>::kN;
   __shared__ Sums sums[kWarps];
   __shared__ uint64_t list[kWarps / 2 * 32];
@@ -199,13 +192,14 @@ __global__ void __launch_bounds__(kThreads, 2) token_logprobs_kernel(const Logpr
   const int64_t chunks = (p.V + skew + N - 1) / N;
   const int64_t c0 = chunks * rank / ctas, c1 = chunks * (rank + 1) / ctas;
 
-  // ---- sums, and the chunk of the largest value
+  // ---- sums, and where the largest value is: kBatch chunks at a time,
+  // kThreads apart, so that the maximum is looked at once for all of them
   Sums a = {-INFINITY, 0.0f, 0.0f};
   int64_t best_chunk = c0 + threadIdx.x;
-  auto add = [&](const float (&v)[N], int64_t c) {
+  auto add = [&](const float *v, int count, int64_t c) {  // (count is a constant where it is called)
     float cm = fmaxf(v[0], v[1]), cl = fminf(v[0], v[1]);
 #pragma unroll
-    for (int e = 2; e < N; e += 2) {
+    for (int e = 2; e < count; e += 2) {
       cm = max3(cm, v[e], v[e + 1]);
       cl = min3(cl, v[e], v[e + 1]);
     }
@@ -218,58 +212,67 @@ __global__ void __launch_bounds__(kThreads, 2) token_logprobs_kernel(const Logpr
       }
       a.m = cm;
     }
-    if (a.m == -INFINITY) {  // only -infinity so far, or NaN
+    if (cl == -INFINITY || a.m == -INFINITY) {  // d e^d of -infinity is 0: with a lower limit
 #pragma unroll
-      for (int e = 0; e < N; ++e)
-        if (v[e] != v[e]) a.s = v[e];
-      return;
-    }
-    if (cl == -INFINITY) {  // d e^d of -infinity is 0: with a lower limit
-#pragma unroll
-      for (int e = 0; e < N; ++e) {
-        const float d = below(v[e], a.m), x = ex2(__fmul_rn(d, kLog2e));
-        a.s += x;
-        a.u = __fmaf_rn(x, d, a.u);
+      for (int e = 0; e < count; ++e) {
+        if (a.m == -INFINITY) {  // only -infinity so far, or NaN
+          if (v[e] != v[e]) a.s = v[e];
+        } else {
+          const float d = below(v[e], a.m), x = ex2(__fmul_rn(d, kLog2e));
+          a.s += x;
+          a.u = __fmaf_rn(x, d, a.u);
+        }
       }
       return;
     }
     const uint64_t minus_m = pair(-a.m, -a.m), log2e = pair(kLog2e, kLog2e);
-    uint64_t s = pair(0.0f, 0.0f), u = s;
+    uint64_t s[2], u[2];
+    s[0] = s[1] = u[0] = u[1] = pair(0.0f, 0.0f);
 #pragma unroll
-    for (int e = 0; e < N; e += 2) {
+    for (int e = 0; e < count; e += 2) {
       const uint64_t d = add2(pair(v[e], v[e + 1]), minus_m);
       float t0, t1;
       unpair(mul2(d, log2e), t0, t1);
       const uint64_t x = pair(ex2(t0), ex2(t1));
-      s = add2(s, x);
-      u = fma2(x, d, u);
+      s[(e >> 1) & 1] = add2(s[(e >> 1) & 1], x);
+      u[(e >> 1) & 1] = fma2(x, d, u[(e >> 1) & 1]);
     }
     float s0, s1;
-    unpair(s, s0, s1);
+    unpair(add2(s[0], s[1]), s0, s1);
     a.s += s0 + s1;
-    unpair(u, s0, s1);
+    unpair(add2(u[0], u[1]), s0, s1);
     a.u += s0 + s1;
   };
+  constexpr int kBatch = 2;
   int64_t c = c0 + threadIdx.x;
-  for (; c + 3 * kThreads < c1; c += 4 * kThreads) {
-    float v[4][N];
+  for (; c + (kBatch - 1) * kThreads < c1; c += kBatch * kThreads) {
+    float v[kBatch * N];
+    if (c > 0 && c + (kBatch - 1) * kThreads < chunks - 1) {  // whole chunks, all loads before the first use
+      uint4 raw[kBatch];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) load_chunk<KIND>(row, c + i * kThreads, skew, p.V, v[i]);
+      for (int i = 0; i < kBatch; ++i)
+        raw[i] = __ldg(reinterpret_cast<const uint4 *>(row - skew * (16 / N)) + c + i * kThreads);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) add(v[i], c + i * kThreads);
+      for (int i = 0; i < kBatch; ++i) values_of<KIND>(raw[i], &v[i * N]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i)
+        load_chunk<KIND>(row, c + i * kThreads, skew, p.V, *reinterpret_cast<float(*)[N]>(&v[i * N]));
+    }
+    add(v, kBatch * N, c);
   }
   for (; c < c1; c += kThreads) {
     float v[N];
     load_chunk<KIND>(row, c, skew, p.V, v);
-    add(v, c);
+    add(v, N, c);
   }
   Sums w = a;
-  w = join_lanes(w, lane);
+  w = join_lanes(w);
   if (lane == 0) sums[warp] = w;
   __syncthreads();
   if (warp == 0) {  // the CTA's
     w = lane < kWarps ? sums[lane] : Sums{-INFINITY, 0.0f, 0.0f};
-    w = join_lanes(w, lane);
+    w = join_lanes(w);
     __syncwarp();
     if (lane == 0) sums[0] = w;
   }
@@ -287,11 +290,15 @@ __global__ void __launch_bounds__(kThreads, 2) token_logprobs_kernel(const Logpr
         k[e] = i >= 0 && i < p.V ? key_of(v[e], static_cast<uint32_t>(i)) : 0;
       }
     };
-    if (best_chunk < c1) {
-      uint64_t k[N];
-      chunk_keys(best_chunk, k);
 #pragma unroll
-      for (int e = 0; e < N; ++e) key = k[e] > key ? k[e] : key;
+    for (int i = 0; i < kBatch; ++i) {
+      const int64_t at = best_chunk + i * kThreads;
+      if (at < c1) {
+        uint64_t k[N];
+        chunk_keys(at, k);
+#pragma unroll
+        for (int e = 0; e < N; ++e) key = k[e] > key ? k[e] : key;
+      }
     }
     if (threadIdx.x == 0) n_winners = 0;
     block_best(sort32(key, lane), list, warp, lane);
@@ -330,7 +337,7 @@ __global__ void __launch_bounds__(kThreads, 2) token_logprobs_kernel(const Logpr
       asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(all.s) : "r"(at + 4) : "memory");
       asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(all.u) : "r"(at + 8) : "memory");
     }
-    all = join_lanes(all, lane);
+    all = join_lanes(all);
     if (p.top > 0) {
       for (uint32_t r = 1; r < ctas; ++r) {
         uint64_t b;
