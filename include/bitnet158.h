@@ -514,7 +514,7 @@ bitnet_status bitnet_kv_attention(const bitnet_kv_cache *cache, const void *Q, v
  *   packed   [N][K / 2] bytes, 16-byte aligned: a little-endian 32-bit word
  *            holds 8 consecutive weights of a row, weight 2i + h of them as
  *            code + 8 at bits [16h + 4i, 16h + 4i + 4).
- *   scales   [N][K / group] bf16, 4-byte aligned.
+ *   scales   [N][K / group] bf16, 16-byte aligned.
  * Quantiser: s = bf16(max |w| / 7) of the group (0 if below 2^-60),
  * code = clamp(round_half_away(w * (1 / s)), -8, 7) (0 for s = 0); weight =
  * code * s.

@@ -145,7 +145,7 @@ bitnet_status bitnet_quantize_weights_w4(const void *W, bitnet_dtype w_dtype, in
     return BITNET_ERR_UNSUPPORTED_SHAPE;
   if (N == 0) return BITNET_OK;
   if (W == nullptr || packed == nullptr || scales == nullptr) return BITNET_ERR_INVALID_ARG;
-  if (!aligned(W, 16) || !aligned(packed, 16) || !aligned(scales, 4)) return BITNET_ERR_MISALIGNED;
+  if (!aligned(W, 16) || !aligned(packed, 16) || !aligned(scales, 16)) return BITNET_ERR_MISALIGNED;
   const uint64_t n = static_cast<uint64_t>(N) * K;
   if (overlap(W, n * float_size(w_dtype), packed, n / 2) ||
       overlap(W, n * float_size(w_dtype), scales, n / group * 2))
@@ -165,7 +165,7 @@ bitnet_status bitnet_w4a16_matmul(const void *X, bitnet_dtype x_dtype, const uin
     return BITNET_ERR_UNSUPPORTED_SHAPE;
   if (M == 0 || N == 0) return BITNET_OK;
   if (X == nullptr || packed == nullptr || scales == nullptr || Y == nullptr) return BITNET_ERR_INVALID_ARG;
-  if (!aligned(X, 16) || !aligned(packed, 16) || !aligned(Y, 16) || !aligned(scales, 4))
+  if (!aligned(X, 16) || !aligned(packed, 16) || !aligned(Y, 16) || !aligned(scales, 16))
     return BITNET_ERR_MISALIGNED;
   if (overlap(X, static_cast<uint64_t>(M) * K * float_size(x_dtype), Y,
               static_cast<uint64_t>(M) * N * float_size(y_dtype)))

@@ -1,4 +1,9 @@
 // attention.cuh -- what the attention kernels over the 8-bit cache share.
+//
+// Here and in the other kernels of the decode step, what an earlier kernel may
+// have written is read through L2 (__ldcg) or by bulk copies: these kernels
+// start before that one has ended (programmatic dependent launch), so nothing
+// of it may come from a cache that was filled meanwhile.
 #pragma once
 
 #include <cuda_fp16.h>
@@ -20,12 +25,12 @@ constexpr float kRaise = 7.0f;
 // do not describe one.  (Rows of queries and positions fit 32 bits: T *
 // q_heads and max_pages * page_tokens are below 2^31.)
 __device__ __forceinline__ bool kv_sequence(const KvBatch &batch, int P, int b, int *r0, int *r1, int *len) {
-  *len = __ldg(batch.lens + b);
+  *len = __ldcg(batch.lens + b);
   *r0 = b;
   *r1 = b + 1;
   if (batch.offsets != nullptr) {
-    *r0 = __ldg(batch.offsets + b);
-    *r1 = __ldg(batch.offsets + b + 1);
+    *r0 = __ldcg(batch.offsets + b);
+    *r1 = __ldcg(batch.offsets + b + 1);
   }
   return *r0 >= 0 && *r1 <= batch.T && *r0 <= *r1 && *len >= 0 && *len <= batch.max_pages * P;
 }

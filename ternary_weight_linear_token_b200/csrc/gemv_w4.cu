@@ -120,8 +120,8 @@ template <int TERMS> struct Raw {
   uint4 v[TERMS == 1 ? 1 : 2];
   __device__ __forceinline__ void load(const void *x, int64_t at) {
     const uint4 *p = reinterpret_cast<const uint4 *>(static_cast<const uint8_t *>(x) + at * (TERMS == 1 ? 2 : 4));
-    v[0] = __ldg(p);
-    if (TERMS != 1) v[TERMS == 1 ? 0 : 1] = __ldg(p + 1);
+    v[0] = __ldcg(p);
+    if (TERMS != 1) v[TERMS == 1 ? 0 : 1] = __ldcg(p + 1);
   }
 };
 // ... and as TERMS rows of bf16: themselves, or the nearest bf16 to what the
@@ -390,8 +390,8 @@ __global__ void __launch_bounds__(kManyWarps * 32, 2) w4_many_kernel(const W4Par
       if (c < c1 && at < groups) {
         wa1[q].load(p.packed + na * (K / 2) + at * (G / 2) + t * (G / 8));
         wb1[q].load(p.packed + nb * (K / 2) + at * (G / 2) + t * (G / 8));
-        sa1[q] = __ldg(p.scales + na * groups + at);
-        sb1[q] = __ldg(p.scales + nb * groups + at);
+        sa1[q] = __ldcg(p.scales + na * groups + at);
+        sb1[q] = __ldcg(p.scales + nb * groups + at);
       }
     }
   };

@@ -52,7 +52,8 @@ struct AttnParams {
   int window;
   int row_tiles, pieces;
   int piece;           // tokens per piece, a multiple of kChunk
-  float *part_o;       // [pieces][T * q_heads][D]; null: one piece, O written here
+  bool cluster;        // the pieces are the CTAs of a cluster, which join them
+  float *part_o;       // else, for several: [pieces][T * q_heads][D] for the joining kernel
   float2 *part_ml;     // [pieces][T * q_heads] (max, sum)
   int *status;
 };
@@ -94,6 +95,16 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
   return y;
 }
 
+// *p of CTA `rank` of the cluster.
+__device__ __forceinline__ float2 peer(const float2 *p, int rank) {
+  float2 v;
+  asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];"
+               : "=f"(v.x), "=f"(v.y)
+               : "r"(mapa_shared(p, static_cast<uint32_t>(rank)))
+               : "memory");
+  return v;
+}
+
 template <typename T> __device__ __forceinline__ T lds(const void *p) { return *static_cast<const T *>(p); }
 
 // One row tile of one piece.  TERMS: columns per query row (1 bf16, 2 fp32);
@@ -121,7 +132,7 @@ __device__ __forceinline__ void attend(const AttnParams &p, uint8_t *smem, int b
   const int query0 = row0 / G, query1 = (row0 + rows - 1) / G;  // of the first and last row
   int lo, hi;
   visible(len, n, query0, query1, p.window, &lo, &hi);
-  if (p.part_o != nullptr) {
+  if (p.pieces > 1) {
     lo = hi - lo > piece_index * p.piece ? lo + piece_index * p.piece : hi;
     if (hi - lo > p.piece) hi = lo + p.piece;
   }
@@ -138,7 +149,7 @@ __device__ __forceinline__ void attend(const AttnParams &p, uint8_t *smem, int b
   const int rounds = (chunks - warp + kWarps - 1) / kWarps;
   auto page_of = [&](int i) -> int {
     const int tok = tok_lane + i * (kWarps * kChunk);
-    return lane < 4 && i < rounds && tok < hi ? __ldg(table + (tok >> page_shift)) : -1;
+    return lane < 4 && i < rounds && tok < hi ? __ldcg(table + (tok >> page_shift)) : -1;
   };
   // ... then its bytes into stage st (pages of 32 tokens and more: the first
   // tile's lanes copy both tiles), and its scale, -1 where there is no page.
@@ -154,7 +165,7 @@ __device__ __forceinline__ void attend(const AttnParams &p, uint8_t *smem, int b
     __syncwarp();
     float s = -1.0f;
     if (ok) {
-      s = __ldg(page_scales + static_cast<int64_t>(page) * p.cache.heads);
+      s = __ldcg(page_scales + static_cast<int64_t>(page) * p.cache.heads);
       if ((copies >> lane) & 1u)
         bulk_g2s(ring + st * R::kStageBytes + (lane >> 1) * R::kBytes + (lane & 1) * (R::kBytes / 2),
                  codes + page * page_bytes + (tok & (P - 1)) * D, bytes, &full[st]);
@@ -208,10 +219,10 @@ __device__ __forceinline__ void attend(const AttnParams &p, uint8_t *smem, int b
         if (have) {
           const int64_t e = at + 64 * c + 16 * t + 4 * i;
           if (TERMS == 2) {
-            const float4 f = __ldg(reinterpret_cast<const float4 *>(static_cast<const float *>(p.q) + e));
+            const float4 f = __ldcg(reinterpret_cast<const float4 *>(static_cast<const float *>(p.q) + e));
             x[0] = f.x; x[1] = f.y; x[2] = f.z; x[3] = f.w;
           } else {
-            const uint2 u = __ldg(reinterpret_cast<const uint2 *>(static_cast<const __nv_bfloat16 *>(p.q) + e));
+            const uint2 u = __ldcg(reinterpret_cast<const uint2 *>(static_cast<const __nv_bfloat16 *>(p.q) + e));
             x[0] = __uint_as_float(u.x << 16); x[1] = __uint_as_float(u.x & 0xFFFF0000u);
             x[2] = __uint_as_float(u.y << 16); x[3] = __uint_as_float(u.y & 0xFFFF0000u);
           }
@@ -473,6 +484,20 @@ __device__ __forceinline__ void attend(const AttnParams &p, uint8_t *smem, int b
       }
     }
   __syncthreads();
+  float *co = reinterpret_cast<float *>(sml + kWarps * kRows);  // the CTA's rows, for its cluster
+  float2 *cml = reinterpret_cast<float2 *>(co + kRows * D);
+  auto row_of = [&](int row) -> int64_t {
+    const int query = (row0 + row) / G;
+    return static_cast<int64_t>(r0 + query) * p.q_heads + h * G + (row0 + row - query * G);
+  };
+  auto store = [&](int64_t out_row, int d, float x, float y, float sum) {
+    const float inv = sum == 0.0f ? 0.0f : __fdiv_rn(1.0f, sum);  // nothing visible: zeros
+    if (TERMS == 2)
+      *reinterpret_cast<float2 *>(static_cast<float *>(p.o) + out_row * D + d) = make_float2(x * inv, y * inv);
+    else
+      *reinterpret_cast<__nv_bfloat162 *>(static_cast<__nv_bfloat16 *>(p.o) + out_row * D + d) =
+          __floats2bfloat162_rn(x * inv, y * inv);
+  };
   for (int i = threadIdx.x; i < kRows * D / 2; i += kWarps * 32) {
     const int row = i / (D / 2), d = i % (D / 2) * 2;
     if (row >= rows) break;
@@ -489,20 +514,37 @@ __device__ __forceinline__ void attend(const AttnParams &p, uint8_t *smem, int b
       y = __fmaf_rn(f, v.y, y);
       sum = __fmaf_rn(f, ml.y, sum);
     }
-    const int query = (row0 + row) / G;
-    const int64_t out_row = static_cast<int64_t>(r0 + query) * p.q_heads + h * G + (row0 + row - query * G);
+    if (p.cluster) {
+      *reinterpret_cast<float2 *>(co + row * D + d) = make_float2(x, y);
+      if (d == 0) cml[row] = make_float2(top, sum);
+      continue;
+    }
+    const int64_t out_row = row_of(row);
     if (p.part_o != nullptr) {
       const int64_t at = static_cast<int64_t>(piece_index) * p.batch.T * p.q_heads + out_row;
       *reinterpret_cast<float2 *>(p.part_o + at * D + d) = make_float2(x, y);
       if (d == 0) p.part_ml[at] = make_float2(top, sum);
     } else {
-      const float inv = sum == 0.0f ? 0.0f : __fdiv_rn(1.0f, sum);  // nothing visible: zeros
-      if (TERMS == 2)
-        *reinterpret_cast<float2 *>(static_cast<float *>(p.o) + out_row * D + d) = make_float2(x * inv, y * inv);
-      else
-        *reinterpret_cast<__nv_bfloat162 *>(static_cast<__nv_bfloat16 *>(p.o) + out_row * D + d) =
-            __floats2bfloat162_rn(x * inv, y * inv);
+      store(out_row, d, x, y, sum);
     }
+  }
+  if (p.cluster) {  // this CTA's share of the rows, over the pieces in order
+    cluster_sync();
+    for (int i = static_cast<int>(threadIdx.x) + piece_index * kWarps * 32; i < rows * D / 2; i += p.pieces * kWarps * 32) {
+      const int row = i / (D / 2), d = i % (D / 2) * 2;
+      float top = -INFINITY;
+      for (int s = 0; s < p.pieces; ++s) top = fmaxf(top, peer(cml + row, s).x);
+      float x = 0.0f, y = 0.0f, sum = 0.0f;
+      for (int s = 0; s < p.pieces; ++s) {
+        const float2 ml = peer(cml + row, s), v = peer(reinterpret_cast<const float2 *>(co + row * D + d), s);
+        const float f = ml.x == -INFINITY ? 0.0f : ex2(ml.x - top);
+        x = __fmaf_rn(f, v.x, x);
+        y = __fmaf_rn(f, v.y, y);
+        sum = __fmaf_rn(f, ml.y, sum);
+      }
+      store(row_of(row), d, x, y, sum);
+    }
+    cluster_sync();  // the others have read this CTA's
   }
 }
 
@@ -635,8 +677,10 @@ __global__ void __launch_bounds__(kWarps * 32) kv_join_kernel(const AttnParams p
 struct AttnPlan {
   int nt, rows;
   int64_t row_tiles, piece, pieces;
+  bool cluster;
 };
 constexpr int64_t kSms = 148;
+constexpr int64_t kClusterSpan = 4096 + 128;
 AttnPlan plan_of(const KvCache &cache, const KvBatch &batch, const AttnArgs &args) {
   AttnPlan a;
   const int terms = args.kind == kF32 ? 2 : 1;
@@ -656,6 +700,17 @@ AttnPlan plan_of(const KvCache &cache, const KvBatch &batch, const AttnArgs &arg
     a.pieces = 1;
     piece = (int64_t(1) << 30);
   }
+  // A short span for few rows: up to 8 pieces as a cluster, which join in the
+  // same launch.  Only while all of them run at once: the CTAs of a cluster
+  // wait for each other.
+  a.cluster = false;
+  if (a.pieces > 1 && span <= kClusterSpan && units * 8 <= kSms * 3) {
+    int64_t size = 2;
+    while (size < 8 && size * 128 < span) size *= 2;
+    a.cluster = true;
+    a.pieces = size;
+    piece = ceil_div(ceil_div(span, size), 128) * 128;
+  }
   a.piece = piece;
   return a;
 }
@@ -669,6 +724,9 @@ cudaError_t launch(const AttnParams &p, const AttnPlan &a, const LaunchCtx &ctx)
   static std::atomic<uint64_t> ready[2];  // bit d: device d allows the kernel its shared memory
   cudaError_t e = allow_smem(kernel, smem, ready[a.nt - 1], ctx);
   if (e != cudaSuccess) return e;
+  if (a.cluster)
+    return launch_k_cluster(kernel, dim3(static_cast<unsigned>(blocks)), dim3(kWarps * 32), smem,
+                            static_cast<unsigned>(a.pieces), ctx, p);
   e = launch_k(kernel, dim3(static_cast<unsigned>(blocks)), dim3(kWarps * 32), smem, ctx, p);
   if (e != cudaSuccess || a.pieces == 1) return e;
   return launch_k(kv_join_kernel<D, TERMS == 2>, dim3(static_cast<unsigned>(p.batch.T * p.q_heads)),
@@ -685,7 +743,7 @@ bool use_prompt(const KvCache &cache, const AttnArgs &args) {
 size_t kv_attention_workspace(const KvCache &cache, const KvBatch &batch, const AttnArgs &args) {
   if (use_prompt(cache, args)) return 0;
   const AttnPlan a = plan_of(cache, batch, args);
-  if (a.pieces == 1) return 0;
+  if (a.pieces == 1 || a.cluster) return 0;
   const size_t rows = static_cast<size_t>(a.pieces) * batch.T * args.q_heads;
   return align256(rows * cache.head_dim * sizeof(float)) + align256(rows * sizeof(float2));
 }
@@ -716,7 +774,8 @@ cudaError_t launch_kv_attention(const KvCache &cache, const KvBatch &batch, cons
   p.pieces = static_cast<int>(a.pieces);
   p.piece = static_cast<int>(a.piece);
   p.status = ctx.status;
-  if (a.pieces > 1) {
+  p.cluster = a.cluster;
+  if (a.pieces > 1 && !a.cluster) {
     const size_t rows = static_cast<size_t>(a.pieces) * batch.T * args.q_heads;
     p.part_o = static_cast<float *>(workspace);
     p.part_ml = reinterpret_cast<float2 *>(static_cast<uint8_t *>(workspace) +

@@ -257,7 +257,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_prompt_kernel(const 
         uint4 v[D / 8];
 #pragma unroll
         for (int c = 0; c < D / 8; ++c)
-          v[c] = have ? __ldg(reinterpret_cast<const uint4 *>(p.q + at) + c) : make_uint4(0, 0, 0, 0);
+          v[c] = have ? __ldcg(reinterpret_cast<const uint4 *>(p.q + at) + c) : make_uint4(0, 0, 0, 0);
         uint32_t peak = 0;
 #pragma unroll
         for (int c = 0; c < D / 8; ++c) {
@@ -451,7 +451,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_prompt_kernel(const 
     const int page_shift = 31 - __clz(P);
     auto page_of = [&](int j) -> int {  // of segment `lane` of block j
       const int tok = lo + j * kTile + 16 * lane;
-      return lane < kSegs && j < total && tok < hi ? __ldg(table + (tok >> page_shift)) : -1;
+      return lane < kSegs && j < total && tok < hi ? __ldcg(table + (tok >> page_shift)) : -1;
     };
     auto checked = [&](int page, int j) -> int {
       if (page >= 0 && page < p.cache.pages) return page;
@@ -462,7 +462,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_prompt_kernel(const 
     auto load16 = [&](int page, int j, int r, int chunk) -> uint4 {
       if (page < 0) return make_uint4(0, 0, 0, 0);
       const int row = (j * kTile + r) & (P - 1);  // (lo is a multiple of every page size)
-      return __ldg(reinterpret_cast<const uint4 *>(head + page * page_bytes + row * D) + chunk);
+      return __ldcg(reinterpret_cast<const uint4 *>(head + page * page_bytes + row * D) + chunk);
     };
     for (int rb = blocks - 1 - from_end; rb >= 0 && ok; rb -= p.row_blocks) {
       enter(rb);
@@ -483,8 +483,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_prompt_kernel(const 
         auto load_scales = [&](int from) {
           ks = -1.0f;
           if (id < kSegs && from >= 0) {
-            ks = __ldg(p.cache.k_scales + static_cast<int64_t>(from) * p.cache.heads + h);
-            vs = __ldg(p.cache.v_scales + static_cast<int64_t>(from) * p.cache.heads + h);
+            ks = __ldcg(p.cache.k_scales + static_cast<int64_t>(from) * p.cache.heads + h);
+            vs = __ldcg(p.cache.v_scales + static_cast<int64_t>(from) * p.cache.heads + h);
           }
         };
         load(page, 0);

@@ -161,7 +161,7 @@ __device__ __forceinline__ void load_chunk(const void *row, int64_t c, int skew,
   constexpr int N = Vec<KIND>::kN;
   const int64_t i0 = c * N - skew;
   if (i0 >= 0 && i0 + N <= V) {
-    values_of<KIND>(__ldg(reinterpret_cast<const uint4 *>(static_cast<const char *>(row) + i0 * (16 / N))), v);
+    values_of<KIND>(__ldcg(reinterpret_cast<const uint4 *>(static_cast<const char *>(row) + i0 * (16 / N))), v);
   } else {
 #pragma unroll
     for (int e = 0; e < N; ++e) {
@@ -251,7 +251,7 @@ __global__ void __launch_bounds__(kThreads, 3) token_logprobs_kernel(const Logpr
       uint4 raw[kBatch];
 #pragma unroll
       for (int i = 0; i < kBatch; ++i)
-        raw[i] = __ldg(reinterpret_cast<const uint4 *>(row - skew * (16 / N)) + c + i * kThreads);
+        raw[i] = __ldcg(reinterpret_cast<const uint4 *>(row - skew * (16 / N)) + c + i * kThreads);
 #pragma unroll
       for (int i = 0; i < kBatch; ++i) values_of<KIND>(raw[i], &v[i * N]);
     } else {

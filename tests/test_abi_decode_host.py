@@ -109,7 +109,7 @@ def test_w4(tw):
         assert quant(**bad) == tw.ERR_INVALID_ARG, bad
     for bad in (dict(g=16), dict(g=256), dict(K=192), dict(K=(1 << 24) + 128), dict(g=0)):
         assert quant(**bad) == tw.ERR_UNSUPPORTED_SHAPE, bad
-    for bad in (dict(W=A + 4), dict(P=B + 8), dict(s=D + 2)):
+    for bad in (dict(W=A + 4), dict(P=B + 8), dict(s=D + 4)):
         assert quant(**bad) == tw.ERR_MISALIGNED, bad
     assert quant(N=0) == tw.OK
 
@@ -120,7 +120,7 @@ def test_w4(tw):
         assert mm(**bad) == tw.ERR_INVALID_ARG, bad
     for bad in (dict(g=96), dict(K=192), dict(K=1 << 25)):
         assert mm(**bad) == tw.ERR_UNSUPPORTED_SHAPE, bad
-    for bad in (dict(X=A + 2), dict(P=B + 4), dict(Y=OFFS + 2), dict(s=D + 1)):
+    for bad in (dict(X=A + 2), dict(P=B + 4), dict(Y=OFFS + 2), dict(s=D + 8)):
         assert mm(**bad) == tw.ERR_MISALIGNED, bad
     assert mm(M=0) == tw.OK and mm(N=0) == tw.OK
     assert mm(M=1 << 20) == tw.ERR_UNSUPPORTED_SHAPE
