@@ -440,7 +440,7 @@ bitnet_status bitnet_decode_chain(const bitnet_chain_step *steps, int n_steps, c
  *            p % page_tokens of page pages[b][p / page_tokens].  Entries
  *            behind a sequence's last position are not read.  Sequences may
  *            share pages that only attention reads; a page that
- *            bitnet_kv_append writes belongs to one sequence.
+ *            bitnet_kv_append writes belongs to one place of one sequence.
  *   lens     [B] int32: tokens of the sequence, the new ones among them.
  *   offsets  [B + 1] int32: rows offsets[b] .. offsets[b + 1] - 1 of the new
  *            tokens' arrays are sequence b's last ones, in order, the last

@@ -14,8 +14,9 @@
 // One CTA owns one (page, head) of K or of V: the scale and the older codes
 // have one writer, and the result does not depend on any order.  The new rows
 // are read once, in 8-element chunks kept in registers between the maximum
-// and the rounding.  Bound by latency for single tokens (three dependent
-// loads: length, page, row) and by HBM for prompts.
+// and the rounding.  Bound by latency: for single tokens by three dependent
+// loads (length, page, scale), for a page of a prompt by one load of its rows
+// and the rounding of each value (8 instructions).
 #include "common.cuh"
 #include "internal.h"
 

@@ -18,7 +18,10 @@
 // (from L2), a lane per chunk.  Warps keep the best 32 keys sorted, one per
 // lane, and join two such lists by a bitonic merge; CTAs of a cluster join
 // theirs through distributed shared memory.
-// Bound by HBM for many rows (one read of the logits), by latency for one.
+// A row of 128256 takes a CTA about 15 us, of which the selection's sorts and
+// barriers are a third: 701 bf16 rows 61 us (2.9 TB/s; three CTAs per SM with
+// batches of 2 chunks against two with batches of 4: 61 against 69 us), one
+// fp32 row over 8 CTAs 12 us, latency.
 #include "common.cuh"
 #include "internal.h"
 #include "pairs.cuh"
