@@ -32,7 +32,8 @@
 // are cut into pieces, which a second kernel joins in piece order; a short one
 // into the CTAs of a cluster, which join by themselves (one launch and no
 // workspace: 10.5 against 14.8 us a call for one sequence of 700 tokens, 15.6
-// against 20.9 for 8 of 4000).
+// against 20.9 for 8 of 4000, 15.6 against 23.5 for 5 drafts each of 16 within
+// a window of 1024).
 // Bound by instruction issue: converting the codes takes some 380 of the 700
 // instructions that a chunk costs with its share of a CTA's start and end.  48
 // sequences of up to 4096 tokens (124 MB): 38 us, 3.3 TB/s; three CTAs per SM
@@ -688,7 +689,7 @@ struct AttnPlan {
   bool cluster;
 };
 constexpr int64_t kSms = 148;
-constexpr int64_t kClusterSpan = 4096 + 128;
+constexpr int64_t kClusterSpan = 4096 + 128, kClusterPiece = 1024 + 32;
 AttnPlan plan_of(const KvCache &cache, const KvBatch &batch, const AttnArgs &args) {
   AttnPlan a;
   const int terms = args.kind == kF32 ? 2 : 1;
@@ -712,12 +713,14 @@ AttnPlan plan_of(const KvCache &cache, const KvBatch &batch, const AttnArgs &arg
   // same launch.  Only while all of them run at once: the CTAs of a cluster
   // wait for each other.
   a.cluster = false;
-  if (a.pieces > 1 && span <= kClusterSpan && units * 8 <= kSms * 3) {
-    int64_t size = 2;
-    while (size < 8 && size * 128 < span) size *= 2;
-    a.cluster = true;
-    a.pieces = size;
-    piece = ceil_div(ceil_div(span, size), 128) * 128;
+  if (a.pieces > 1 && span <= kClusterSpan) {
+    int64_t size = 1;
+    while (size < 8 && size * 128 < span && units * size * 2 <= kSms * 3) size *= 2;
+    if (size > 1 && span <= size * kClusterPiece) {
+      a.cluster = true;
+      a.pieces = size;
+      piece = ceil_div(ceil_div(span, size), 128) * 128;
+    }
   }
   a.piece = piece;
   return a;
