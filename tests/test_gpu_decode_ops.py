@@ -267,6 +267,24 @@ def test_attention_what_is_masked_does_not_count(bl, new):
     assert torch.equal(first, again)
 
 
+@pytest.mark.parametrize("Hq,H,P,D,lens,new,window,hint", [
+    (2, 1, 64, 128, [700, 10], [700, 4], 0, 130),          # more row blocks than the hint tells of
+    (4, 2, 16, 64, [900, 300], [600, 290], 150, 70),
+    (3, 1, 32, 64, [1300], [500], 0, 500),                 # a long prefix
+    (5, 1, 128, 128, [400, 0, 1], [90, 0, 1], 1, 90),
+])
+def test_attention_of_long_prompts(bl, Hq, H, P, D, lens, new, window, hint):
+    rng = np.random.default_rng(Hq + P + D + sum(lens))
+    table, pages = table_of(rng, lens, P)
+    parts = filled(rng, pages, H, P, D)
+    q = dev(rng.standard_normal((sum(new), Hq, D)).astype(np.float32)).bfloat16()
+    for most in (hint, max(new)):
+        o = bl.bitnet_kv_attention(cache_of(bl, parts), q, i32(table), i32(lens), offsets=i32(offsets_of(new)),
+                                   max_new=most, window=window)
+        check_attention(q, o, parts, table, lens, new, window=window)
+    assert bl.bitnet_get_device_status() == bl.OK
+
+
 def test_attention_nan_query_stays_in_its_row(bl):
     rng = np.random.default_rng(9)
     lens, new = [70, 200], [3, 20]
