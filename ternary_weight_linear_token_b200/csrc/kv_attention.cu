@@ -675,10 +675,11 @@ __global__ void __launch_bounds__(kWarps * 32) kv_join_kernel(const AttnParams p
       z += sums[w];
     }
     const float out = z == 0.0f ? 0.0f : __fdiv_rn(y, z);  // nothing visible: zeros
+    const int64_t at = static_cast<int64_t>(row) * D + d;    // (rows fit 32 bits, values don't)
     if (F32)
-      static_cast<float *>(p.o)[row * D + d] = out;
+      static_cast<float *>(p.o)[at] = out;
     else
-      static_cast<__nv_bfloat16 *>(p.o)[row * D + d] = __float2bfloat16_rn(out);
+      static_cast<__nv_bfloat16 *>(p.o)[at] = __float2bfloat16_rn(out);
   }
 }
 
