@@ -40,6 +40,10 @@ bitnet_status check_cache(const bitnet_kv_cache *c) {
   return BITNET_OK;
 }
 
+// A window past every position is the same as one of 2^31 - 1 (and a sum with
+// it must not overflow).
+int64_t window_of(int64_t window) { return window < kMaxCount ? window : kMaxCount; }
+
 // Sizes of a batch; then, where it has rows, its arrays.
 bitnet_status check_batch_sizes(int64_t T, int64_t B, int64_t max_pages, const int32_t *offsets,
                                 int64_t max_new, const bitnet_kv_cache *cache) {
@@ -105,7 +109,7 @@ size_t bitnet_kv_attention_workspace_size(const bitnet_kv_cache *cache, bitnet_d
   if (check_attention(cache, dtype, T, q_heads, B, max_pages, &some, max_new, window) != BITNET_OK ||
       T == 0 || B == 0)
     return 0;
-  const AttnArgs args = {nullptr, nullptr, dtype, q_heads, 1.0f, window, max_new};
+  const AttnArgs args = {nullptr, nullptr, dtype, q_heads, 1.0f, window_of(window), max_new};
   const KvBatch batch = {nullptr, nullptr, nullptr, max_pages, B, T};
   return kv_attention_fits(cache_of(cache), batch, args) ? kv_attention_workspace(cache_of(cache), batch, args) : 0;
 }
@@ -124,7 +128,7 @@ bitnet_status bitnet_kv_attention(const bitnet_kv_cache *cache, const void *Q, v
   if (!aligned(Q, 16) || !aligned(O, 16)) return BITNET_ERR_MISALIGNED;
   const uint64_t bytes = static_cast<uint64_t>(T) * q_heads * cache->head_dim * float_size(dtype);
   if (overlap(Q, bytes, O, bytes)) return BITNET_ERR_INVALID_ARG;
-  const AttnArgs args = {Q, O, dtype, q_heads, scale, window, max_new};
+  const AttnArgs args = {Q, O, dtype, q_heads, scale, window_of(window), max_new};
   const KvBatch batch = {pages, lens, offsets, max_pages, B, T};
   const KvCache c = cache_of(cache);
   if (!kv_attention_fits(c, batch, args)) return BITNET_ERR_UNSUPPORTED_SHAPE;

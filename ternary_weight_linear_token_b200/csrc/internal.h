@@ -182,7 +182,7 @@ struct AttnArgs {
   void *O;
   int kind, q_heads;
   float scale;
-  int64_t window;   // 0: none
+  int64_t window;   // 0: none; below 2^31
   int64_t max_new;
 };
 size_t kv_attention_workspace(const KvCache &cache, const KvBatch &batch, const AttnArgs &args);

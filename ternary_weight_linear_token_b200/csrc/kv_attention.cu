@@ -781,7 +781,7 @@ cudaError_t launch_kv_attention(const KvCache &cache, const KvBatch &batch, cons
   p.q_heads = args.q_heads;
   p.group = args.q_heads / cache.heads;
   p.scale_log2 = args.scale * kLog2e;
-  p.window = static_cast<int>(args.window < (int64_t(1) << 31) - 1 ? args.window : (int64_t(1) << 31) - 1);
+  p.window = static_cast<int>(args.window);
   p.row_tiles = static_cast<int>(a.row_tiles);
   p.pieces = static_cast<int>(a.pieces);
   p.piece = static_cast<int>(a.piece);

@@ -672,7 +672,7 @@ cudaError_t launch_kv_attention_prompt(const KvCache &cache, const KvBatch &batc
   p.group = args.q_heads / cache.heads;
   p.negate = args.scale < 0.0f;
   p.scale_log2 = (p.negate ? -args.scale : args.scale) * kLog2e;
-  p.window = static_cast<int>(args.window < (int64_t(1) << 31) - 1 ? args.window : (int64_t(1) << 31) - 1);
+  p.window = static_cast<int>(args.window);
   p.row_blocks = static_cast<int>(ceil_div(args.max_new * p.group, 2 * kTile));
   p.status = ctx.status;
   const dim3 grid(static_cast<unsigned>(batch.B * p.row_blocks * cache.heads));

@@ -97,6 +97,17 @@ def test_attention(tw):
     assert size(C.addressof(c), 1, 0, 20, 0, 1000, 1, 0) == 0
 
 
+def test_attention_largest_windows(tw):
+    """Windows past every position, the largest there are among them, cut a call as no window does."""
+    c = cache(tw)
+    size = tw.lib.bitnet_kv_attention_workspace_size
+    for n in (1, 2, 8):
+        none = size(C.addressof(c), 1, n, 20, n, 1000, 1, 0)
+        assert none > 0
+        for window in (64000, 1 << 30, (1 << 31) - 1, 1 << 31, 1 << 62, (1 << 63) - 1):
+            assert size(C.addressof(c), 1, n, 20, n, 1000, 1, window) == none
+
+
 def test_w4(tw):
     q = tw.lib.bitnet_quantize_weights_w4
     ok = dict(W=A, dt=0, N=4, K=256, g=128, P=B, s=D)
