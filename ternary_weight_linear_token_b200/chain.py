@@ -37,7 +37,7 @@ from __future__ import annotations
 
 import torch
 
-from . import (bitnet_decode_chain, bitnet_decode_chain_steps, bitnet_decode_chain_workspace_size,
+from . import (KVCache, bitnet_decode_chain, bitnet_decode_chain_steps, bitnet_decode_chain_workspace_size,
                bitnet_kv_append, bitnet_kv_attention, bitnet_kv_attention_workspace_size,
                bitnet_quantize_weights, bitnet_quantize_weights_w4, bitnet_rms_norm,
                bitnet_rms_norm_w158a8_matmul, bitnet_token_logprobs, bitnet_w158a8_matmul,
@@ -196,20 +196,39 @@ class DecodeChain:
 
     def capture(self) -> torch.cuda.CUDAGraph:
         """Capture one token through the whole stack in a CUDA graph.  (With
-        caches the warm-up writes the next token's place, which the next run
-        writes again.)"""
+        caches the warm-up is the first token of a cache of its own, into
+        buffers of its own: nothing of the sequence changes.)"""
         s = torch.cuda.Stream(self.device)
         s.wait_stream(torch.cuda.current_stream(self.device))
         with torch.cuda.stream(s):
-            self.run()  # warm-up outside capture
-            if self.caches is not None:
-                self.lens.sub_(1)
+            self._warm_up()
         torch.cuda.current_stream(self.device).wait_stream(s)
         g = torch.cuda.CUDAGraph()
         with torch.cuda.graph(g):
             self.run()
         self.graph = g
         return g
+
+    def _warm_up(self) -> None:
+        """Runs a token outside capture.  An append would leave its mark on the
+        caches that taking the length back does not remove: a page's scale that
+        grew, and its older tokens' codes rounded to it."""
+        if self.caches is None:
+            self.run()
+            return
+        c = self.caches[0]
+        kept = dict(vars(self))
+        try:
+            self.caches = [KVCache(1, c.page_tokens, c.heads, c.head_dim, device=self.device)] * len(self.caches)
+            self.pages = torch.zeros_like(self.pages)  # as wide as the sequence's: the same kernels
+            self.lens = torch.zeros_like(self.lens)
+            self.outs = [[torch.empty_like(t) for t in bufs] for bufs in self.outs]
+            self.attended = [torch.empty_like(t) for t in self.attended]
+            if self.head is not None:
+                self.logits = torch.empty_like(self.logits)
+            self.run()
+        finally:
+            vars(self).update(kept)
 
     def launches_per_token(self) -> int:
         head = 0 if self.head is None else 1

@@ -95,6 +95,34 @@ def test_captured_and_replayed(bl):
     assert eager.launches_per_token() == 2 * (4 + 2) + 2 and bl.bitnet_get_device_status() == bl.OK
 
 
+@pytest.mark.parametrize("ran,page_tokens,pages", [(21, 16, 3), (16, 16, 3), (32, 16, 2)])
+def test_capture_leaves_no_trace(bl, ran, page_tokens, pages):
+    """Captured after some tokens, in the middle of a page, at its end and on a full cache, with a large
+    token left in x_in: caches, links, logits, length and status stay as they were, and what follows is
+    what an eager chain gives."""
+    eager, chain = (chain_of(bl, pages=pages, page_tokens=page_tokens) for _ in range(2))
+    xs = tokens_of(ran + 6)
+    for x in xs[:ran]:
+        eager.run(x)
+        chain.run(x)
+    chain.x_in.copy_(xs[0] * 1000)
+
+    def state(c):
+        return ([t for k in c.caches for t in (k.k_codes, k.k_scales, k.v_codes, k.v_scales)]
+                + [t for bufs in c.outs for t in bufs] + c.attended + [c.logits, c.lens])
+    before = [t.clone() for t in state(chain)]
+    graph = chain.capture()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(state(chain), before))
+    assert bl.bitnet_get_device_status() == bl.OK
+    for x in xs[ran:min(ran + 6, pages * page_tokens)]:
+        eager.run(x)
+        chain.x_in.copy_(x)
+        graph.replay()
+        assert all(torch.equal(a, b) for a, b in zip(state(chain), state(eager)))
+    assert bl.bitnet_get_device_status() == bl.OK
+
+
 def test_two_chains_at_once(bl):
     """Two sequences on two streams, graphs of both in flight together, give what each gives alone."""
     alone = [chain_of(bl, seed=s) for s in (0, 1)]
