@@ -215,7 +215,9 @@ __global__ void __launch_bounds__(kThreads, 3) token_logprobs_kernel(const Logpr
       }
       a.m = cm;
     }
-    if (cl == -INFINITY || a.m == -INFINITY) {  // d e^d of -infinity is 0: with a lower limit
+    // d = -infinity (a value of -infinity, or a finite one too far below the
+    // maximum): d e^d counts as 0, by a lower limit for d
+    if (cl - a.m == -INFINITY || a.m == -INFINITY) {
 #pragma unroll
       for (int e = 0; e < count; ++e) {
         if (a.m == -INFINITY) {  // only -infinity so far, or NaN

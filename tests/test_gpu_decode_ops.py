@@ -488,6 +488,32 @@ def test_logprobs_of_difficult_rows(bl, dtype):
         check_logprobs(x[m:m + 1], tokens[m:m + 1], top, bl.bitnet_token_logprobs(x[m:m + 1], tokens[m:m + 1], top=top))
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_logprobs_of_values_far_apart(bl, dtype):
+    """Finite values whose distance to the row's maximum is no fp32 number, before and after the maximum."""
+    low = torch.finfo(dtype).min
+    x = torch.randn(6, 9000, device=DEV).to(dtype)
+    x[0, 7], x[0, 8000] = 2e32, low
+    x[1], x[1, 8999] = low, 3e38
+    x[2], x[2, ::3] = -3e38, 3e38
+    x[3], x[3, 5] = low, 1e31
+    x[4, ::7] = low          # an ordinary row, some of it masked by the lowest value
+    x[5], x[5, 1] = 1e38, low
+    tokens = dev(np.array([7, 0, 1, 5, 3, 1]))
+    lp, h, ids, tl = ref.logprobs(x.double().cpu().numpy(), tokens.cpu().numpy(), 5)
+    with np.errstate(over="ignore"):  # below fp32's lowest number: rounded to -infinity
+        lp, tl = lp.astype(np.float32), tl.astype(np.float32)
+    steps = (9000 / 4096 + 32 + 40) * 2.0 ** -23  # as in check_logprobs
+    for rows in [slice(0, 6)] + [slice(m, m + 1) for m in range(6)]:
+        glp, gh, gids, gtl = (t.cpu().numpy() for t in bl.bitnet_token_logprobs(x[rows], tokens[rows], top=5))
+        assert np.array_equal(gids, ids[rows])
+        for got, want in ((glp, lp[rows]), (gtl, tl[rows])):
+            assert np.array_equal(got == -np.inf, want == -np.inf)
+            fine = want != -np.inf
+            assert (np.abs(got[fine] - want[fine]) <= steps + (np.abs(want[fine]) + 14) * 2.0 ** -21).all()
+        assert (np.abs(gh - h[rows]) <= steps + (np.abs(h[rows]) * 4 + 14) * 2.0 ** -21).all()
+
+
 def test_logprobs_nan_and_tokens_that_are_not_there(bl):
     x = torch.randn(4, 5000, device=DEV)
     x[1, 77] = torch.nan
