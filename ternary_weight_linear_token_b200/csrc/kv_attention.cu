@@ -246,7 +246,7 @@ __device__ __forceinline__ void attend(const AttnParams &p, uint8_t *smem, int b
     peak = fmaxf(peak, __shfl_xor_sync(0xffffffffu, peak, 2));
     // 2^k brings the row's largest value into [2^14, 2^15)
     int k = 14 - (static_cast<int>(__float_as_uint(peak) >> 23) - 127);
-    k = k < -110 ? -110 : (k > 110 ? 110 : k);
+    k = k < -113 ? -113 : (k > 110 ? 110 : k);  // (finite ones need -113 at least)
     const float up = __uint_as_float(static_cast<uint32_t>(127 + k) << 23);
     const float f = __fmul_rn(p.scale_log2, __uint_as_float(static_cast<uint32_t>(127 - k) << 23));
 #pragma unroll

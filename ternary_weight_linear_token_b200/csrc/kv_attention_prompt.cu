@@ -276,7 +276,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_prompt_kernel(const 
           }
         }
         int k = 14 - (static_cast<int>(peak >> 23) - 127);
-        k = k < -110 ? -110 : (k > 110 ? 110 : k);
+        k = k < -113 ? -113 : (k > 110 ? 110 : k);  // (finite ones need -113 at least)
         const float up = __uint_as_float((static_cast<uint32_t>(127 + k) << 23) | (p.negate ? 0x80000000u : 0u));
         fac = __fmul_rn(p.scale_log2, __uint_as_float(static_cast<uint32_t>(127 - k) << 23));
         uint8_t *tile = smem + S::kQ + t * S::kOperand;

@@ -1,11 +1,11 @@
 """The decode step's operators where their numbers and sizes end: rows past
-2^31 values.  Tolerances as in test_gpu_decode_ops."""
+2^31 values, the largest queries.  Tolerances as in test_gpu_decode_ops."""
 
 import numpy as np
 import pytest
 import torch
 
-from test_gpu_decode_ops import DEV, cache_of, check_attention, dev, filled, i32
+from test_gpu_decode_ops import DEV, cache_of, check_attention, dev, filled, i32, offsets_of, table_of
 
 pytestmark = pytest.mark.gpu
 
@@ -35,3 +35,24 @@ def test_attention_joined_rows_past_2_31_values(bl):
     bl.bitnet_kv_attention(cache_of(bl, parts), Q, i32(table), i32([200]), offsets=i32([T - 1, T]), max_new=1, O=O)
     check_attention(Q[-1:], O[-1:], parts, table, [200], [1])
     assert (O[[0, T // 2, T - 2]] == 7).all() and bl.bitnet_get_device_status() == bl.OK
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("n", [1, 60])
+def test_attention_of_the_largest_queries(bl, dtype, n):
+    """Queries up to 0.99 * 2^128, with keys and a scale that make ordinary scores of them."""
+    rng = np.random.default_rng(n)
+    H, P, D, Hq = 2, 16, 64, 8
+    lens, new = [150, 97], [n, 1]
+    table, pages = table_of(rng, lens, P)
+    parts = filled(rng, pages, H, P, D)
+    parts[1] *= np.float32(2.0 ** -40)
+    q = np.clip(rng.standard_normal((sum(new), Hq, D)), -3.9, 3.9) / 4
+    q[:, :, 0] = 0.99
+    for e in (125, 126, 127, 128):
+        x = dev(np.ldexp(q, e).astype(np.float32)).to(dtype)
+        assert x.isfinite().all()
+        scale = 2.0 ** (40 - e)
+        o = bl.bitnet_kv_attention(cache_of(bl, parts), x, i32(table), i32(lens), offsets=i32(offsets_of(new)),
+                                   max_new=n, scale=scale)
+        check_attention(x, o, parts, table, lens, new, scale=scale)
