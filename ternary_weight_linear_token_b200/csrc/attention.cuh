@@ -45,6 +45,29 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
+// 2^x down to fp32's smallest number (2^-149).
+__device__ __forceinline__ float ex2_whole(float x) {
+  float y;
+  asm("ex2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// Value scales far apart.  A weight p' = 2^(score + log2 vs - m + kRaise)
+// counts for O only next to the largest p', but its share p' / vs of the row
+// sum counts next to the other shares: with vs = 2^-59 (or a page of zeros,
+// log2 vs = -60) beside vs = 2^60, p' can be below 2^-126 where p' / vs is the
+// larger share.  As long as vs stays within 2^-30 and 2^30, such a share is
+// below 2^-66 of the largest.  Where one does not, shares are taken as
+// 2^(score - m + kRaise) by an exponential of their own.
+__device__ __forceinline__ bool far_scale(float vs) {  // (infinite: what sees it is NaN anyway)
+  return vs < 9.313225746154785e-10f || (vs > 1073741824.0f && vs < INFINITY);
+}
+// v * 2^d where 2^d alone is below 2^-126 (a share can be 2^75).
+__device__ __forceinline__ float times_ex2(float v, float d) {
+  const float half = ex2(__fmul_rn(d, 0.5f));
+  return __fmul_rn(__fmul_rn(v, half), half);
+}
+
 __device__ __forceinline__ uint32_t half2_bits(__half2 h) {
   return *reinterpret_cast<uint32_t *>(&h);
 }

@@ -21,9 +21,10 @@
 // vs enters as log2(vs) added to the score: p' = 2^(s + log2 vs - m) with the
 // running maximum m of that sum, so O += p' vc needs no further scale, while
 // the row sum adds p' / vs.  A page of zeros (vs = 0) counts with log2 vs =
-// -60.  p' is held 2^kRaise higher, and m may lag behind by kLazy: p' stays
-// below 2^15, and fp16 rounds it by at most 2^-12 of itself or, below fp16's
-// normal numbers, by 2^-25: 2^-32 of the largest weight.
+// -60 (scales far apart: attention.cuh).  p' is held 2^kRaise higher, and m may
+// lag behind by kLazy: p' stays below 2^15, and fp16 rounds it by at most 2^-12
+// of itself or, below fp16's normal numbers, by 2^-25: 2^-32 of the largest
+// weight.
 //
 // A CTA's 4 warps take every 4th chunk of 32 tokens of its piece of the
 // sequence, each with its own ring of chunks filled by bulk copies (K and V
@@ -114,12 +115,21 @@ __device__ __forceinline__ float2 peer(const float2 *p, int rank) {
   return v;
 }
 
+// sum + f ml.y of a part with maximum and row sum ml, f = 2^(ml.x - top) (0
+// for a part without a maximum); f can be 0 where the product is not.
+__device__ __forceinline__ float add_share(float sum, float2 ml, float top, float f) {
+  sum = __fmaf_rn(f, ml.y, sum);
+  if (f == 0.0f && ml.y > 0.0f) sum += times_ex2(ml.y, ml.x - top);
+  return sum;
+}
+
 template <typename T> __device__ __forceinline__ T lds(const void *p) { return *static_cast<const T *>(p); }
 
 // One row tile of one piece.  TERMS: columns per query row (1 bf16, 2 fp32);
-// NT: column tiles of 8.
-template <int D, int TERMS, int NT>
-__device__ __forceinline__ void attend(const AttnParams &p, uint8_t *smem, int b, int h, int row_tile,
+// NT: column tiles of 8.  APART: for value scales far apart (attention.cuh);
+// the other form returns true when it has met some, and has stored nothing.
+template <int D, int TERMS, int NT, bool APART>
+__device__ __forceinline__ bool attend(const AttnParams &p, uint8_t *smem, int b, int h, int row_tile,
                                        int piece_index, int r0, int n, int len, uint32_t &phase,
                                        int &stage) {
   using R = Ring<D>;
@@ -146,7 +156,7 @@ __device__ __forceinline__ void attend(const AttnParams &p, uint8_t *smem, int b
     if (hi - lo > p.piece) hi = lo + p.piece;
   }
   const int chunks = hi > lo ? (hi - lo + kChunk - 1) / kChunk : 0;
-  if (chunks == 0 && p.part_o != nullptr) return;  // the joining kernel knows
+  if (chunks == 0 && p.part_o != nullptr) return false;  // the joining kernel knows
 
   // Lanes 0-3 fetch the chunk of the warp's round i (tile = lane & 1, K or V =
   // lane >> 1): the page number (-1 where there is none), ...
@@ -181,6 +191,7 @@ __device__ __forceinline__ void attend(const AttnParams &p, uint8_t *smem, int b
     }
     return s;
   };
+  bool far = false;  // lanes 2, 3: a scale far from others
   auto keep_scale = [&](int st, float s) {
     ChunkScales &k = scales[st];
     if (lane < 2) k.ks[lane] = s;
@@ -188,7 +199,10 @@ __device__ __forceinline__ void attend(const AttnParams &p, uint8_t *smem, int b
       // s = 0: a page of zeros; s < 0: no page, its tokens are not seen
       const bool some = !(s < kKvMinScale);
       k.lv[lane & 1] = some ? log2f(s) : -60.0f;
-      k.iv[lane & 1] = some ? __fdiv_rn(1.0f, s) : 1.152921504606846976e18f;  // 2^60
+      if (!APART) {
+        far |= s >= 0.0f && far_scale(s);
+        k.iv[lane & 1] = some ? __fdiv_rn(1.0f, s) : 1.0f;
+      }
     }
   };
 
@@ -205,7 +219,11 @@ __device__ __forceinline__ void attend(const AttnParams &p, uint8_t *smem, int b
       if (i < rounds) s[i] = issue(i, page[i], (stage + i) % R::kStages);
 #pragma unroll
     for (int i = 0; i < R::kStages; ++i)
-      if (i < rounds) keep_scale((stage + i) % R::kStages, s[i]);
+      if (i < rounds) {
+        // (a first tile that no row sees must not count as a scale far from the others)
+        const bool unseen = i == 0 && lane == 2 && tok_lane + 16 <= first_seen(len - n + query0, p.window);
+        keep_scale((stage + i) % R::kStages, unseen ? 1.0f : s[i]);
+      }
   }
 
   // q as B fragments: column g of column tile j is row j * 8 / TERMS + g / TERMS
@@ -378,8 +396,8 @@ __device__ __forceinline__ void attend(const AttnParams &p, uint8_t *smem, int b
         for (int r = 0; r < kPer; ++r) {
           const float to = fmaxf(m[j][r], top[j][r]);
           f[r] = m[j][r] == to ? 1.0f : ex2(m[j][r] - to);
+          l[j][r] = APART && f[r] == 0.0f && l[j][r] > 0.0f ? times_ex2(l[j][r], m[j][r] - to) : l[j][r] * f[r];
           m[j][r] = to;
-          l[j][r] *= f[r];
         }
 #pragma unroll
         for (int s = 0; s < kSteps; ++s)
@@ -396,7 +414,13 @@ __device__ __forceinline__ void attend(const AttnParams &p, uint8_t *smem, int b
       for (int r = 0; r < kPer; ++r) from[j][r] = m[j][r] == -INFINITY ? 0.0f : m[j][r] - kRaise;
 #pragma unroll
     for (int tile = 0; tile < 2; ++tile) {
-      const float iv = scales[st].iv[tile];
+      const float lv = APART ? scales[st].lv[tile] : 0.0f, iv = APART ? 0.0f : scales[st].iv[tile];
+      auto share = [&](float weight, float score, float &sum) {
+        if (APART)
+          sum += ex2_whole(score - lv);
+        else
+          sum = __fmaf_rn(weight, iv, sum);
+      };
       uint32_t pf[NT][2];
 #pragma unroll
       for (int j = 0; j < NT; ++j)
@@ -405,7 +429,7 @@ __device__ __forceinline__ void attend(const AttnParams &p, uint8_t *smem, int b
           __half2 x;
           if (TERMS == 2) {
             const float a = ex2(s2[tile][j][0][e] - from[j][0]);
-            l[j][0] = __fmaf_rn(a, iv, l[j][0]);
+            share(a, s2[tile][j][0][e] - from[j][0], l[j][0]);
             const float hi_part = __half2float(__float2half_rn(a));
             x = __floats2half2_rn(hi_part, a - hi_part);
           } else {
@@ -413,7 +437,7 @@ __device__ __forceinline__ void attend(const AttnParams &p, uint8_t *smem, int b
 #pragma unroll
             for (int r = 0; r < kPer; ++r) {
               a[r] = ex2(s2[tile][j][r][e] - from[j][r]);
-              l[j][r] = __fmaf_rn(a[r], iv, l[j][r]);
+              share(a[r], s2[tile][j][r][e] - from[j][r], l[j][r]);
             }
             x = __floats2half2_rn(a[0], a[kPer - 1]);
           }
@@ -471,7 +495,7 @@ __device__ __forceinline__ void attend(const AttnParams &p, uint8_t *smem, int b
       l[j][r] += __shfl_xor_sync(0xffffffffu, l[j][r], 8);
       l[j][r] += __shfl_xor_sync(0xffffffffu, l[j][r], 16);
     }
-  __syncthreads();  // the rings are idle
+  if (__syncthreads_or(far)) return true;  // (the rings are idle)
   float *so = reinterpret_cast<float *>(smem);
   float2 *sml = reinterpret_cast<float2 *>(so + kWarps * kRows * D);
 #pragma unroll
@@ -521,7 +545,7 @@ __device__ __forceinline__ void attend(const AttnParams &p, uint8_t *smem, int b
       const float2 v = *reinterpret_cast<const float2 *>(so + (w * kRows + row) * D + d);
       x = __fmaf_rn(f, v.x, x);
       y = __fmaf_rn(f, v.y, y);
-      sum = __fmaf_rn(f, ml.y, sum);
+      sum = APART ? add_share(sum, ml, top, f) : __fmaf_rn(f, ml.y, sum);
     }
     if (p.cluster) {
       *reinterpret_cast<float2 *>(co + row * D + d) = make_float2(x, y);
@@ -549,16 +573,31 @@ __device__ __forceinline__ void attend(const AttnParams &p, uint8_t *smem, int b
         const float f = ml.x == -INFINITY ? 0.0f : ex2(ml.x - top);
         x = __fmaf_rn(f, v.x, x);
         y = __fmaf_rn(f, v.y, y);
-        sum = __fmaf_rn(f, ml.y, sum);
+        sum = add_share(sum, ml, top, f);
       }
       store(row_of(row), d, x, y, sum);
     }
     cluster_sync();  // the others have read this CTA's
   }
+  return false;
+}
+
+// The form for value scales far apart.  (A function of its own, so that the
+// other form keeps its registers: 39.4 against 40.5 us for 48 sequences of up
+// to 4096 tokens.)
+struct RingState {
+  uint32_t phase;
+  int stage;
+};
+template <int D, int TERMS, int NT>
+__device__ __noinline__ RingState attend_apart(const AttnParams &p, uint8_t *smem, int b, int h, int row_tile,
+                                               int piece_index, int r0, int n, int len, RingState ring) {
+  attend<D, TERMS, NT, true>(p, smem, b, h, row_tile, piece_index, r0, n, len, ring.phase, ring.stage);
+  return ring;
 }
 
 template <int D, int TERMS, int NT>
-__global__ void __launch_bounds__(kWarps * 32, 3) kv_attention_kernel(const AttnParams p) {
+__global__ void __launch_bounds__(kWarps * 32, 3) kv_attention_kernel(const __grid_constant__ AttnParams p) {
   extern __shared__ __align__(128) uint8_t smem[];
   using R = Ring<D>;
   uint64_t *full = reinterpret_cast<uint64_t *>(
@@ -586,7 +625,11 @@ __global__ void __launch_bounds__(kWarps * 32, 3) kv_attention_kernel(const Attn
   uint32_t phase = 0;  // bit s: the parity of the warp's stage s to wait for next
   int stage = 0;       // its next stage
   for (int rt = first_tile; rt < tiles; rt += p.row_tiles) {
-    attend<D, TERMS, NT>(p, smem, b, h, rt, piece, r0, n, len, phase, stage);
+    if (attend<D, TERMS, NT, false>(p, smem, b, h, rt, piece, r0, n, len, phase, stage)) {
+      const RingState ring = attend_apart<D, TERMS, NT>(p, smem, b, h, rt, piece, r0, n, len, {phase, stage});
+      phase = ring.phase;
+      stage = ring.stage;
+    }
     fence_proxy_async_smem();  // the joined sums lie where the next bulk copies go
     __syncthreads();
   }
@@ -648,10 +691,10 @@ __global__ void __launch_bounds__(kWarps * 32) kv_join_kernel(const AttnParams p
     const float f = ml.x == -INFINITY ? (ml.y == 0.0f ? 0.0f : ml.y) : ex2(ml.x - to);
     weight[threadIdx.x] = f;
     __syncthreads();
-    float part = f * ml.y;
+    float part = f == 0.0f && ml.y > 0.0f ? times_ex2(ml.y, ml.x - to) : f * ml.y;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) part += __shfl_xor_sync(0xffffffffu, part, o);
-    sum = __fmaf_rn(sum, old, part);  // of this warp's pieces
+    sum = old == 0.0f && sum > 0.0f ? times_ex2(sum, top - to) + part : __fmaf_rn(sum, old, part);  // this warp's
     top = to;
 #pragma unroll
     for (int e = 0; e < kPer; ++e) x[e] *= old;

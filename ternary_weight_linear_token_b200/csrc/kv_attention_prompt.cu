@@ -68,7 +68,8 @@ struct PromptParams {
 };
 
 struct BlockScales {
-  float ks[kSegs], lv[kSegs], iv[kSegs];  // ks < 0: no page
+  // ks < 0: no page, iv = 0; iv < 0: value scales far apart, here or before (attention.cuh)
+  float ks[kSegs], lv[kSegs], iv[kSegs];
 };
 
 template <int D> struct Smem {
@@ -152,6 +153,76 @@ template <int N> __device__ __forceinline__ void more_registers() {
 }
 template <int N> __device__ __forceinline__ void fewer_registers() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+// A block of the softmax below with value scales far apart: every score
+// compared with the mask, shares of the row sum by themselves, rescaled in two
+// steps (l may be 2^75, f 2^-181).  Its own function, so that the form for
+// scales as they should be keeps its registers (236 against 227 us for prompts
+// of 4096 tokens).
+struct Row {
+  float m, l;
+  bool ok;
+};
+template <int D>
+__device__ __noinline__ Row far_block(Row r, uint32_t ts, uint32_t to, float fac, const BlockScales &sc, int c_lo,
+                                      int c_hi, uint64_t *pv_done, uint32_t parity, int *status) {
+  // score + log2 vs of column c, -infinity where it is not seen
+  auto score = [&](uint32_t v, int c, float plus) -> float {
+    const float ks = sc.ks[c / 16];
+    return c < c_lo || c >= c_hi || ks < 0.0f ? -INFINITY
+                                              : __fmaf_rn(__uint_as_float(v), __fmul_rn(fac, fabsf(ks)), plus);
+  };
+  float top = -INFINITY;
+#pragma unroll 1
+  for (int c0 = 0; c0 < kTile; c0 += 16) {
+    uint32_t v[16];
+    tmem_ld16(ts + c0, v);
+    tmem_arrived(v);
+#pragma unroll
+    for (int e = 0; e < 16; ++e) top = fmaxf(top, score(v[e], c0 + e, sc.lv[c0 / 16]));
+  }
+  const bool grow = top > r.m + kLazy;
+  if (__any_sync(0xffffffffu, grow)) {
+    const float next = grow ? ceilf(top) : r.m;
+    const int steps = r.m == next ? 0 : static_cast<int>(fmaxf(r.m - next, -250.0f)), half = steps / 2;
+    const float f0 = __uint_as_float(static_cast<uint32_t>(127 + half) << 23);
+    const float f1 = __uint_as_float(static_cast<uint32_t>(127 + steps - half) << 23);
+    r.m = next;
+    r.l = __fmul_rn(__fmul_rn(r.l, f0), f1);
+    if (pv_done != nullptr) {  // there is an O
+      r.ok = wait_for(pv_done, parity, status);
+      r.ok = __all_sync(0xffffffffu, r.ok);
+      if (!r.ok) return r;
+      tc_fence_after();
+#pragma unroll 1
+      for (int e = 0; e < D / 16; ++e) {
+        uint32_t o[16];
+        tmem_ld16(to + 16 * e, o);
+        tmem_arrived(o);
+#pragma unroll
+        for (int z = 0; z < 16; ++z)
+          o[z] = __float_as_uint(__fmul_rn(__fmul_rn(__uint_as_float(o[z]), f0), f1));
+        tmem_st16(to + 16 * e, o);
+      }
+    }
+  }
+  const float from = r.m == -INFINITY ? 0.0f : kRaise - r.m;
+#pragma unroll 1
+  for (int c0 = 0; c0 < kTile; c0 += 32) {
+    uint32_t v[32], w[16];
+    tmem_ld32(ts + c0, v);
+    tmem_arrived(v);
+#pragma unroll
+    for (int e = 0; e < 32; e += 2) {
+      const int c = c0 + e;
+      const float lv = sc.lv[c / 16];
+      r.l += ex2_whole(score(v[e], c, from)) + ex2_whole(score(v[e + 1], c + 1, from));
+      w[e / 2] = half2_bits(__floats2half2_rn(ex2(score(v[e], c, lv + from)), ex2(score(v[e + 1], c + 1, lv + from))));
+    }
+    tmem_st16(ts + c0 / 2, w);
+  }
+  return r;
 }
 
 template <int D>
@@ -311,7 +382,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_prompt_kernel(const 
         const int c_hi = pos + 1 - (lo + j * kTile), c_lo = first - (lo + j * kTile);
         bool part = c_hi < kTile || c_lo > 0;
 #pragma unroll
-        for (int s = 0; s < kSegs; ++s) part |= sc.ks[s] < 0.0f;
+        for (int s = 0; s < kSegs; ++s) part |= !(sc.iv[s] > 0.0f);
         // Twice over the scores, 32 columns at a time with the next ones on
         // their way: the row's maximum; then weights, written over scores that
         // have been read, and their sum.  A block that every row of the warp
@@ -407,7 +478,22 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_prompt_kernel(const 
           }
           return true;
         };
-        ok = __any_sync(0xffffffffu, part) ? weights(std::true_type{}) : weights(std::false_type{});
+        if (!__any_sync(0xffffffffu, part)) {
+          ok = weights(std::false_type{});
+        } else {
+          bool apart = false;
+#pragma unroll
+          for (int s = 0; s < kSegs; ++s) apart |= sc.iv[s] < 0.0f;
+          if (apart) {
+            const Row r = far_block<D>({m, l, true}, ts, to, fac, sc, c_lo, c_hi, j > 0 ? &pv_done[t] : nullptr,
+                                       (tj - 1) & 1, p.status);
+            m = r.m;
+            l = r.l;
+            ok = r.ok;
+          } else {
+            ok = weights(std::true_type{});
+          }
+        }
         if (!ok) break;
         tmem_wait_st();
         tc_fence_before();
@@ -486,6 +572,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_prompt_kernel(const 
           }
         };
         float ks = -1.0f, vs = 0.0f;  // of segment `lane`, the first warp's
+        bool apart = false;           // a value scale far from others so far
         auto load_scales = [&](int from) {
           ks = -1.0f;
           if (id < kSegs && from >= 0) {
@@ -495,6 +582,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_prompt_kernel(const 
         };
         load(page, 0);
         load_scales(page);
+        // (a page that no row sees must not count as a scale far from the others)
+        if (lo + 16 * lane + 16 <= first_seen(len - n + row0 / G, p.window)) vs = 1.0f;
         for (int j = 0; j < total; ++j) {
           const int st = stage(j);
           if (use(j) > 0) {  // the stage's last user has gone through
@@ -507,10 +596,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_prompt_kernel(const 
             // come before those of block j - 2 that k_empty waits for)
             BlockScales &sc = scales[(done + j) % kSlots];
             if (lane < kSegs) {
-              const bool some = ks >= 0.0f && !(vs < kKvMinScale);
               sc.ks[lane] = ks;
-              sc.lv[lane] = some ? log2f(vs) : -60.0f;
-              sc.iv[lane] = some ? __fdiv_rn(1.0f, vs) : 1.152921504606846976e18f;  // 2^60
+              sc.lv[lane] = vs < kKvMinScale ? -60.0f : log2f(vs);
+              apart |= ks >= 0.0f && far_scale(vs);
+              sc.iv[lane] = apart ? -1.0f : ks < 0.0f ? 0.0f : __fdiv_rn(1.0f, vs);
             }
             mbar_arrive(&sc_full[(done + j) % kSlots]);
           }

@@ -1,5 +1,6 @@
 """The decode step's operators where their numbers and sizes end: rows past
-2^31 values, the largest queries.  Tolerances as in test_gpu_decode_ops."""
+2^31 values, the largest queries, value
+scales far apart.  Tolerances as in test_gpu_decode_ops."""
 
 import numpy as np
 import pytest
@@ -56,3 +57,54 @@ def test_attention_of_the_largest_queries(bl, dtype, n):
         o = bl.bitnet_kv_attention(cache_of(bl, parts), x, i32(table), i32(lens), offsets=i32(offsets_of(new)),
                                    max_new=n, scale=scale)
         check_attention(x, o, parts, table, lens, new, scale=scale)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("lens,new,P", [([150], [1], 16), ([150], [60], 16), ([5000], [1], 128),
+                                        ([300] * 24, [1] * 24, 32), ([700], [200], 64)])
+@pytest.mark.parametrize("large", [20, 40, 61, 100, 119])
+def test_attention_value_scales_far_apart(bl, dtype, lens, new, P, large):
+    """Pages of zeros, of values near 2^-59 and of huge ones side by side, in any order: the small ones count
+    in the row sum as they should."""
+    rng = np.random.default_rng(large + sum(lens))
+    H, D, Hq = 2, 64, 8
+    table, pages = table_of(rng, lens, P)
+    parts = filled(rng, pages, H, P, D)
+    for b in range(len(lens)):
+        held = -(-lens[b] // P)
+        kind = rng.integers(0, 4, held)
+        kind[:3] = rng.permutation(3)
+        for k, p in zip(kind, table[b, :held]):
+            if k == 0:
+                parts[2][p], parts[3][p] = 0, 0
+            elif k == 1:
+                parts[3][p] = 2.0 ** large
+            elif k == 2:
+                parts[3][p] = 2.0 ** -59
+    q = dev(rng.standard_normal((sum(new), Hq, D)).astype(np.float32)).to(dtype)
+    o = bl.bitnet_kv_attention(cache_of(bl, parts), q, i32(table), i32(lens), offsets=i32(offsets_of(new)),
+                               max_new=max(new))
+    check_attention(q, o, parts, table, lens, new)
+    assert bl.bitnet_get_device_status() == bl.OK
+
+
+@pytest.mark.parametrize("new", [[1, 1, 1], [40, 1, 25]])
+def test_attention_scales_of_unseen_pages(bl, new):
+    """Huge and tiny value scales of pages before every row's window change nothing."""
+    rng = np.random.default_rng(8)
+    H, P, D, Hq, window = 1, 16, 128, 4, 40
+    lens = [100, 85, 77]
+    table, pages = table_of(rng, lens, P)
+    parts = filled(rng, pages, H, P, D)
+    q = dev(rng.standard_normal((sum(new), Hq, D)).astype(np.float32))
+    args = dict(offsets=i32(offsets_of(new)), max_new=max(new), window=window)
+    used = set()
+    for b, (n, t) in enumerate(zip(lens, new)):
+        used |= set(table[b, max(0, n - t - window + 1) // P: (n - 1) // P + 1].tolist())
+    unseen = sorted(set(range(pages)) - used)
+    assert len(unseen) > 2
+    other = parts[:3] + [parts[3].copy()]
+    other[3][unseen[::2]], other[3][unseen[1::2]] = 2.0 ** 100, 2.0 ** -59
+    for x in (q, q.bfloat16()):
+        a, b = (bl.bitnet_kv_attention(cache_of(bl, p), x, i32(table), i32(lens), **args) for p in (parts, other))
+        assert torch.equal(a, b)
