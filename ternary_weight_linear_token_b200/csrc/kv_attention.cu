@@ -201,7 +201,8 @@ __device__ __forceinline__ bool attend(const AttnParams &p, uint8_t *smem, int b
       k.lv[lane & 1] = some ? log2f(s) : -60.0f;
       if (!APART) {
         far |= s >= 0.0f && far_scale(s);
-        k.iv[lane & 1] = some ? __fdiv_rn(1.0f, s) : 1.0f;
+        // (a weight of 0 must stay 0: no NaN where the page is masked)
+        k.iv[lane & 1] = some && s < INFINITY ? __fdiv_rn(1.0f, s) : 1.0f;
       }
     }
   };

@@ -599,7 +599,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_prompt_kernel(const 
               sc.ks[lane] = ks;
               sc.lv[lane] = vs < kKvMinScale ? -60.0f : log2f(vs);
               apart |= ks >= 0.0f && far_scale(vs);
-              sc.iv[lane] = apart ? -1.0f : ks < 0.0f ? 0.0f : __fdiv_rn(1.0f, vs);
+              // (a weight of 0 must stay 0: no NaN where the page is masked)
+              sc.iv[lane] = apart ? -1.0f : ks < 0.0f ? 0.0f : vs < INFINITY ? __fdiv_rn(1.0f, vs) : 1.0f;
             }
             mbar_arrive(&sc_full[(done + j) % kSlots]);
           }

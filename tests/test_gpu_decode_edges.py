@@ -108,3 +108,31 @@ def test_attention_scales_of_unseen_pages(bl, new):
     for x in (q, q.bfloat16()):
         a, b = (bl.bitnet_kv_attention(cache_of(bl, p), x, i32(table), i32(lens), **args) for p in (parts, other))
         assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("new", [[3, 1, 4], [40, 1, 25]])
+def test_attention_scales_that_are_no_numbers(bl, dtype, new):
+    """A NaN or infinite scale of the last page: rows before that page, in the same tiles as rows that see
+    it, stay as they were; with NaN the others are NaN."""
+    rng = np.random.default_rng(8)
+    H, P, D, Hq = 1, 16, 128, 4
+    lens = [99, 45, 35]
+    table, pages = table_of(rng, lens, P)
+    parts = filled(rng, pages, H, P, D)
+    q = dev(rng.standard_normal((sum(new), Hq, D)).astype(np.float32)).to(dtype)
+    args = dict(offsets=i32(offsets_of(new)), max_new=max(new))
+    first = bl.bitnet_kv_attention(cache_of(bl, parts), q, i32(table), i32(lens), **args)
+    pos = np.concatenate([np.arange(n - t, n) for n, t in zip(lens, new)])
+    edge = np.repeat([(n - 1) // P * P for n in lens], new)
+    before = torch.from_numpy(pos < edge).to(DEV)
+    assert before.any() and not before.all()
+    for bad in (np.nan, np.inf):
+        for i in (1, 3):
+            other = [a.copy() for a in parts]
+            for b, n in enumerate(lens):
+                other[i][table[b, (n - 1) // P]] = bad
+            o = bl.bitnet_kv_attention(cache_of(bl, other), q, i32(table), i32(lens), **args)
+            assert torch.equal(o[before], first[before])
+            if np.isnan(bad):
+                assert o[~before].isnan().all()
