@@ -40,13 +40,9 @@ __device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// Weights 2i and 2i + 1 of a word as two bf16, 136 too large.
-__device__ __forceinline__ uint32_t two_biased(uint32_t w, int i) {
-  return ((w >> (4 * i)) & 0x000F000Fu) | 0x43004300u;
-}
-// The same, exactly.
+// Weights 2i and 2i + 1 of a word as two bf16.
 __device__ __forceinline__ uint32_t two_codes(uint32_t w, int i) {
-  const uint32_t x = two_biased(w, i), bias = 0x43084308u;  // 136, twice
+  const uint32_t x = ((w >> (4 * i)) & 0x000F000Fu) | 0x43004300u, bias = 0x43084308u;  // 136, twice
   const __nv_bfloat162 v = __hsub2(*reinterpret_cast<const __nv_bfloat162 *>(&x),
                                    *reinterpret_cast<const __nv_bfloat162 *>(&bias));
   return *reinterpret_cast<const uint32_t *>(&v);
@@ -180,10 +176,10 @@ template <int G> struct Words {
 // are a tile ahead in shared memory (two stages: a third costs a CTA per SM
 // and time, 55 against 49 us for 128256 x 2560), each warp over every 4th
 // group; the warps' sums meet in shared memory, one barrier per tile, which
-// also hands the stage back.  The unpack is what the SM has to issue: bf16
-// activations skip its subtraction (7 instructions per 8 weights instead of
-// 11) and take 136 times the group's activation sum away afterwards, an fp32
-// error of 30 units of the group's sum at most.
+// also hands the stage back.  Codes are made exact before the products: taking
+// 136 times the group's activation sum away afterwards saves 4 of 11
+// instructions per 8 weights and 0.6 of 50.2 us, but its error grows with the
+// largest activation, whatever that one's code is.
 constexpr int kFewWarps = 4, kFewStages = 2;
 constexpr size_t kFewSmem = 112 * 1024;  // of a CTA, two per SM
 struct FewPlan {
@@ -193,7 +189,7 @@ struct FewPlan {
 // false: the tiles are too long
 inline bool few_plan(int64_t M, int64_t K, int group, int terms, FewPlan *f) {
   const int64_t groups = K / group;
-  const int64_t x = terms * (M + 1) * (K + 8) * 2 + (terms == 1 ? 8 * groups * 4 : 0), w = 8 * K, s = 32 * groups;
+  const int64_t x = terms * (M + 1) * (K + 8) * 2, w = 8 * K, s = 32 * groups;
   const int64_t x16 = (x + 15) / 16 * 16, stage = w + s;
   if (x16 + kFewStages * stage + 64 > static_cast<int64_t>(kFewSmem)) return false;
   f->x_bytes = static_cast<int>(x16);
@@ -212,7 +208,6 @@ __global__ void __launch_bounds__(kFewWarps * 32) w4_few_kernel(const W4Params p
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int K = static_cast<int>(p.K), groups = K / G, M = static_cast<int>(p.M), pitch = K + 8;
   __nv_bfloat16 *xs = reinterpret_cast<__nv_bfloat16 *>(smem);       // [TERMS][M + 1][pitch], the last row 0
-  float *xsum = reinterpret_cast<float *>(smem + TERMS * (M + 1) * pitch * 2);  // [8][groups]
   uint8_t *ring = smem + f.x_bytes;
   uint64_t *full = reinterpret_cast<uint64_t *>(ring + f.stages * f.stage_bytes);
   if (threadIdx.x < f.stages) mbar_init(&full[threadIdx.x], 1);
@@ -253,24 +248,6 @@ __global__ void __launch_bounds__(kFewWarps * 32) w4_few_kernel(const W4Params p
 #pragma unroll
     for (int k = 0; k < TERMS; ++k) *reinterpret_cast<uint4 *>(xs + (k * (M + 1) + m) * pitch + c * 8) = v[k];
   }
-  if (TERMS == 1) {
-    __syncthreads();
-    for (int i = threadIdx.x; i < 8 * groups; i += kFewWarps * 32) {
-      const int m = i / groups, q = i - m * groups;
-      float s = 0.0f;
-      if (m < M) {
-        const uint4 *src = reinterpret_cast<const uint4 *>(xs + m * pitch + q * G);
-#pragma unroll 4
-        for (int e = 0; e < G / 8; ++e) {
-          const uint4 v = src[e];
-          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-          for (int z = 0; z < 4; ++z) s += __uint_as_float(w[z] << 16) + __uint_as_float(w[z] & 0xFFFF0000u);
-        }
-      }
-      xsum[i] = -136.0f * s;
-    }
-  }
   __syncthreads();
 
   const __nv_bfloat16 *x_lane = xs + (g < M ? g : M) * pitch + t * (G / 4);
@@ -296,17 +273,13 @@ __global__ void __launch_bounds__(kFewWarps * 32) w4_few_kernel(const W4Params p
       float c[2][4];  // two chains of sums
 #pragma unroll
       for (int e = 0; e < 4; ++e) c[0][e] = c[1][e] = 0.0f;
-      if (TERMS == 1) {
-        c[0][0] = c[0][2] = xsum[(2 * t) * groups + q];
-        c[0][1] = c[0][3] = xsum[(2 * t + 1) * groups + q];
-      }
 #pragma unroll
       for (int i = 0; i < kWords; ++i) {
         uint32_t fa[4], fb[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          fa[e] = TERMS == 1 ? two_biased(wa.w[i], e) : two_codes(wa.w[i], e);
-          fb[e] = TERMS == 1 ? two_biased(wb.w[i], e) : two_codes(wb.w[i], e);
+          fa[e] = two_codes(wa.w[i], e);
+          fb[e] = two_codes(wb.w[i], e);
         }
 #pragma unroll
         for (int k = TERMS - 1; k >= 0; --k) {

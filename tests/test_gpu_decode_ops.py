@@ -409,6 +409,27 @@ def test_w4_matmul(bl, x_dtype, M, N, K, group):
         check_w4(x, y, codes, s.float().numpy(), group)
 
 
+@pytest.mark.parametrize("x_dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("M", [1, 8, 9])
+def test_w4_matmul_outliers(bl, x_dtype, M):
+    """Large activations on codes of 0, single ones and a group of them under a scale that is not 0, add
+    nothing: the tolerance goes by sum |x w|."""
+    rng = np.random.default_rng(M)
+    N, K, group = 40, 1280, 128
+    codes = rng.integers(-8, 8, (N, K))
+    s = np.full((N, K // group), 0.25, dtype=np.float32)
+    codes[:, [3 * group + 5, 9 * group + 64]] = 0
+    codes[:, 4 * group:5 * group] = 0
+    for size in (1e3, 1e4, 1e5, 1e6, 3e38):
+        x = rng.standard_normal((M, K)).astype(np.float32)
+        x[:, 3 * group + 5] = size
+        x[:, 9 * group + 64] = -size
+        x[:, 4 * group:5 * group] *= size / 8
+        x = dev(x).to(x_dtype)
+        y = bl.bitnet_w4a16_matmul(x, dev(ref.pack_w4(codes)), dev(s).bfloat16(), out_dtype=torch.float32)
+        check_w4(x, y, codes, s, group)
+
+
 def test_w4_matmul_rows_are_their_own(bl):
     """A NaN in one token or an infinity in one scale stays in its row or column; a scale of 0 is 0."""
     rng = np.random.default_rng(5)
