@@ -1,11 +1,13 @@
 """The decode step's operators where their numbers and sizes end: rows past
-2^31 values, the largest queries, value
-scales far apart.  Tolerances as in test_gpu_decode_ops."""
+2^31 values, the largest queries and activations, value scales far apart or no
+numbers, the low bits of fp32.  Tolerances as in test_gpu_decode_ops where none
+is given."""
 
 import numpy as np
 import pytest
 import torch
 
+import decode_ref as ref
 from test_gpu_decode_ops import DEV, cache_of, check_attention, dev, filled, i32, offsets_of, table_of
 
 pytestmark = pytest.mark.gpu
@@ -136,3 +138,78 @@ def test_attention_scales_that_are_no_numbers(bl, dtype, new):
             assert torch.equal(o[before], first[before])
             if np.isnan(bad):
                 assert o[~before].isnan().all()
+
+
+@pytest.mark.parametrize("Hq,H,P,D,lens,new", [
+    (8, 2, 16, 64, [20, 3], [1, 1]),
+    (4, 1, 32, 128, [31], [5]),
+    (3, 3, 128, 64, [9, 24, 2], [2, 7, 1]),
+])
+def test_attention_low_bits_of_fp32(bl, Hq, H, P, D, lens, new):
+    """fp32 queries and weights keep 22 bits.  Each query has one element, so that a score is one product:
+    |log2 score| <= 4 is off by 4 (2^-22 + 2^-23 + 2 * 2^-24) + 2^-22 and by two roundings of 2^-21 next to
+    the maximum (up to 16), with ex2 below 2^-18.8; a weight by that times ln 2, twice (its own and the
+    normaliser's), 2^-22 for its two halves, a sum of 32 by 2^-20: below 2^-17 in all.  Weights or queries of
+    one half are off by more."""
+    rng = np.random.default_rng(D + P)
+    table, pages = table_of(rng, lens, P)
+    parts = filled(rng, pages, H, P, D)
+    parts[1][:], parts[3][:] = 2.0 ** -5, 1.0
+    T = sum(new)
+    q = np.zeros((T, Hq, D), dtype=np.float32)
+    at = rng.integers(0, D, (T, Hq))
+    size = rng.uniform(0.5, 1, (T, Hq)) * rng.choice([-1, 1], (T, Hq))
+    np.put_along_axis(q, at[..., None], size[..., None].astype(np.float32), -1)
+    args = (*parts, table, lens, new, 0.6)
+    want, mass, score, _ = ref.attention(q, *args)
+    assert score.max() * np.log2(np.e) <= 4
+    o = bl.bitnet_kv_attention(cache_of(bl, parts), dev(q), i32(table), i32(lens), offsets=i32(offsets_of(new)),
+                               max_new=max(new), scale=0.6)
+    tol = 2.0 ** -17 * mass
+    assert (np.abs(o.cpu().numpy() - want) <= tol).all()
+    one_half = ref.attention(q.astype(np.float16).astype(np.float32), *args)[0]
+    assert (np.abs(one_half - want) > tol).any()
+    assert (np.abs(one_half_weights(q, *args) - want) > tol).any()
+
+
+def one_half_weights(q, kc, ks, vc, vs, table, lens, new, scale):
+    """What weights rounded once to fp16, their sum exact, would give."""
+    o = np.zeros(q.shape)
+    H, P = kc.shape[1:3]
+    for b, (r0, t, n) in enumerate(ref.rows_of(lens, new)):
+        k, v = (np.concatenate([c[p] * s[p][:, None, None].astype(np.float64) for p in table[b, :-(-n // P)]], 1)
+                for c, s in ((kc, ks), (vc, vs)))
+        for i in range(t):
+            for h in range(q.shape[1]):
+                g, seen = h // (q.shape[1] // H), n - t + i + 1
+                s = scale * (k[g, :seen] @ q[r0 + i, h].astype(np.float64))
+                w = np.exp(s - s.max()) * 128
+                o[r0 + i, h] = w.astype(np.float16).astype(np.float64) @ v[g, :seen] / w.sum()
+    return o
+
+
+# ---------------------------------------------------------------- 4-bit weights
+@pytest.mark.parametrize("M", [1, 4, 9, 23])
+@pytest.mark.parametrize("group", [32, 64, 128])
+def test_w4_matmul_low_bits_of_fp32(bl, M, group):
+    """fp32 activations keep 24 bits.  Rows of one code: its product's three terms add up with one rounding to
+    24 bits, which may truncate: 2^-23 of it.  Rows of two codes that cancel but for the low bits: three
+    roundings more, at the size of one product.  Two terms of 16 bits would be off by more."""
+    rng = np.random.default_rng(M + group)
+    N, K = 48, 384
+    codes = np.zeros((N, K), dtype=np.int64)
+    size = np.zeros(N)
+    for n in range(N):
+        a, b = rng.choice(K, 2, replace=False)
+        codes[n, a] = c = rng.choice([-7, -5, -3, -1, 1, 2, 3, 5, 6, 7])
+        if n % 2:
+            codes[n, b] = -c
+        size[n] = abs(c) * (4 if n % 2 else 1)
+    x = (1 + rng.integers(0, 1 << 22, (M, K)) * 2.0 ** -22 + 2.0 ** -23).astype(np.float32)
+    s = torch.ones(N, K // group, dtype=torch.bfloat16, device=DEV)
+    y = bl.bitnet_w4a16_matmul(dev(x), dev(ref.pack_w4(codes)), s, out_dtype=torch.float32).cpu().numpy()
+    want = x.astype(np.float64) @ codes.T
+    tol = 2.0 ** -23 * 2 * size  # |x| < 2
+    assert (np.abs(y - want) <= tol).all()
+    high = (x.view(np.uint32) & 0xFFFFFF00).view(np.float32)
+    assert (np.abs(high.astype(np.float64) @ codes.T - want) > tol).any()
