@@ -523,7 +523,8 @@ bitnet_status bitnet_quantize_weights_w4(const void *W, bitnet_dtype w_dtype, in
                                          int32_t group, uint8_t *packed, void *scales, bitnet_stream_t stream);
 
 /* Y [M][N] = X [M][K] times the transpose of those weights; X and Y fp32 or
- * bf16 each, 16-byte aligned, not overlapping.  Codes are exact, sums fp32.
+ * bf16 each, 16-byte aligned, not overlapping.  Codes are exact, sums fp32
+ * (a group's sum of x * code before its scale: from 2^128 on it is infinite).
  * X is finite; fp32 X runs as three bf16 terms (24 bits).  flags: 0 or
  * BITNET_FLAG_WEIGHTS_STATIC (packed and scales are not written by the kernel
  * before this call).  Made for few tokens; more run in blocks of 32 that read

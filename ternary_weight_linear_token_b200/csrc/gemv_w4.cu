@@ -122,8 +122,8 @@ template <int TERMS> struct Raw {
     if (TERMS != 1) v[TERMS == 1 ? 0 : 1] = __ldcg(p + 1);
   }
 };
-// ... and as TERMS rows of bf16: themselves, or the nearest bf16 to what the
-// terms before leave of the fp32 value.
+// ... and as TERMS rows of bf16: themselves, or 8 bits of the fp32 value each,
+// cut off (rounding would take the largest ones to infinity).
 template <int TERMS>
 __device__ __forceinline__ void split(const Raw<TERMS> &raw, uint4 (&out)[TERMS]) {
   if (TERMS == 1) {
@@ -137,10 +137,10 @@ __device__ __forceinline__ void split(const Raw<TERMS> &raw, uint4 (&out)[TERMS]
       uint32_t w[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * e], v[2 * e + 1]);
-        w[e] = *reinterpret_cast<const uint32_t *>(&h);
-        v[2 * e] = __fsub_rn(v[2 * e], __low2float(h));
-        v[2 * e + 1] = __fsub_rn(v[2 * e + 1], __high2float(h));
+        const uint32_t lo = __float_as_uint(v[2 * e]), hi = __float_as_uint(v[2 * e + 1]);
+        w[e] = __byte_perm(lo, hi, 0x7632);
+        v[2 * e] = __fsub_rn(v[2 * e], __uint_as_float(lo & 0xFFFF0000u));
+        v[2 * e + 1] = __fsub_rn(v[2 * e + 1], __uint_as_float(hi & 0xFFFF0000u));
       }
       out[t] = make_uint4(w[0], w[1], w[2], w[3]);
     }

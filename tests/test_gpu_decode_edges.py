@@ -213,3 +213,22 @@ def test_w4_matmul_low_bits_of_fp32(bl, M, group):
     assert (np.abs(y - want) <= tol).all()
     high = (x.view(np.uint32) & 0xFFFFFF00).view(np.float32)
     assert (np.abs(high.astype(np.float64) @ codes.T - want) > tol).any()
+
+
+@pytest.mark.parametrize("M", [1, 8, 9])
+def test_w4_matmul_largest_activations(bl, M):
+    """Finite activations up to the largest of their type: a row of one code each, exact but for one rounding.
+    A group's sum of x * code is fp32 and comes before the scale: from 2^128 on it is infinite."""
+    N, K, group = 14, 256, 64
+    codes = np.zeros((N, K), dtype=np.int64)
+    codes[np.arange(N), 17 * np.arange(N)] = [c for c in range(-7, 8) if c != 0]
+    s = torch.full((N, K // group), 2.0 ** -10, dtype=torch.bfloat16, device=DEV)
+    packed = dev(ref.pack_w4(codes))
+    for dtype in (torch.float32, torch.bfloat16):
+        for value in (torch.finfo(dtype).max, 3.39e38, 2.6e36, -torch.finfo(dtype).max):
+            x = torch.full((M, K), value, device=DEV).to(dtype)
+            y = bl.bitnet_w4a16_matmul(x, packed, s, out_dtype=torch.float32).double().cpu().numpy()
+            want = x.double().cpu().numpy() @ codes.T * 2.0 ** -10
+            fits = np.abs(want) < 2.0 ** 118
+            assert (np.abs(y - want)[fits] <= 2.0 ** -23 * np.abs(want)[fits]).all() and fits.any()
+            assert (y[~fits] == np.inf * np.sign(want[~fits])).all()
