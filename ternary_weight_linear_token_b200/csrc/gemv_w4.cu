@@ -255,7 +255,7 @@ __global__ void __launch_bounds__(kFewWarps * 32) w4_few_kernel(const W4Params p
   uint32_t phase = 0;
   for (int tile = blockIdx.x; tile < p.tiles; tile += gridDim.x) {
     const bool ok = mbar_wait(&full[stage], phase, nullptr);  // (recorded below)
-    if (!ok && threadIdx.x == 0) record_status(p.status, kStatusTimeout);
+    if (!ok) record_status(p.status, kStatusTimeout);
     const uint8_t *w = ring + stage * f.stage_bytes + g * (K / 2) + t * (G / 8);
     const uint16_t *s = reinterpret_cast<const uint16_t *>(ring + stage * f.stage_bytes + f.w_bytes) + g * groups;
     int s8 = 8 * groups;  // to the scales of row g + 8
@@ -299,7 +299,12 @@ __global__ void __launch_bounds__(kFewWarps * 32) w4_few_kernel(const W4Params p
     mine[g][2 * t + 1] = y[1];
     mine[g + 8][2 * t] = y[2];
     mine[g + 8][2 * t + 1] = y[3];
-    if (__syncthreads_or(!ok)) return;  // (nothing that gave up is stored)
+    if (__syncthreads_or(!ok)) {  // nothing that gave up is stored; the copies under way end first (with a limit)
+      if (threadIdx.x == 0)
+        for (int i = 0; i < f.stages && tile + static_cast<int64_t>(i) * gridDim.x < p.tiles; ++i)
+          mbar_wait(&full[(stage + i) % f.stages], stage + i < f.stages ? phase : phase ^ 1u, nullptr);
+      return;
+    }
     if (threadIdx.x == 0 && tile + static_cast<int64_t>(f.stages) * gridDim.x < p.tiles)
       copy(tile + f.stages * static_cast<int>(gridDim.x), stage);
     const int row = threadIdx.x % kRows, col = threadIdx.x / kRows;

@@ -313,7 +313,20 @@ __device__ __forceinline__ bool attend(const AttnParams &p, uint8_t *smem, int b
     const int st = stage;
     stage = stage + 1 == R::kStages ? 0 : stage + 1;
     const bool ok = wait_for(&full[st], (phase >> st) & 1u, p.status);
-    if (!__all_sync(0xffffffffu, ok)) break;
+    if (!__all_sync(0xffffffffu, ok)) {  // the copies under way end first (again with a limit); the rows are NaN
+#pragma unroll 1
+      for (int k = 0; k < R::kStages && i + k < rounds; ++k) {
+        stage = (st + k) % R::kStages;
+        wait_for(&full[stage], (phase >> stage) & 1u, p.status);
+        phase ^= 1u << stage;
+      }
+      stage = (stage + 1) % R::kStages;
+#pragma unroll
+      for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int r = 0; r < kPer; ++r) l[j][r] = __uint_as_float(0x7FC00000u);
+      break;
+    }
     phase ^= 1u << st;
     const uint8_t *kt = ring + st * R::kStageBytes;
     const uint8_t *vt = kt + R::kBytes;

@@ -77,7 +77,7 @@ template <int D> struct Smem {
   static constexpr int kQ = 0, kK = 2 * kOperand, kV = kK + kStages * kOperand;
   static constexpr int kScales = kV + kStages * kOperand;
   static constexpr int kBars = kScales + kSlots * static_cast<int>(sizeof(BlockScales));
-  static constexpr int kNumBars = 1 + 4 * kStages + kSlots + 3 * 2;
+  static constexpr int kNumBars = 1 + 4 * kStages + kSlots + 3 * 2 + 1;
   static constexpr size_t kBytes = 1024 + kBars + 8 * kNumBars + 16;
 };
 
@@ -237,7 +237,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_prompt_kernel(const 
   uint64_t *v_full = k_empty + kStages, *v_empty = v_full + kStages;
   uint64_t *sc_full = v_empty + kStages;                       // [kSlots]
   uint64_t *s_full = sc_full + kSlots, *p_full = s_full + 2, *pv_done = p_full + 2;
-  uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(pv_done + 2);
+  uint64_t *drained = pv_done + 2;
+  uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(drained + 1);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
@@ -254,6 +255,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_prompt_kernel(const 
       mbar_init(&p_full[t], kTile);
       mbar_init(&pv_done[t], 1);
     }
+    mbar_init(drained, 1);
     fence_barrier_init();
   }
   if (warp == kMmaWarp) {
@@ -736,6 +738,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_prompt_kernel(const 
       }
       ok = leave(ok);
       q_phase ^= 1u;
+    }
+    if (!ok && warp == kMmaWarp && lane == 0) {  // a wait gave up: the products under way end first
+      mma_commit(drained);
+      wait_for(drained, 0, p.status);
     }
   }
   tc_fence_before();
