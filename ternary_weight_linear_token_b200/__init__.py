@@ -516,11 +516,6 @@ def _same_device(device: int, **tensors):
             raise ValueError(f"{name} must be on cuda:{device}, it is on {t.device}")
 
 
-def _is(t: torch.Tensor, name: str, *dtypes):
-    if t.dtype not in dtypes:
-        raise TypeError(f"{name} must have dtype in {dtypes}, got {t.dtype}")
-
-
 def _dense(t: torch.Tensor, name: str, *dtypes):
     if t.dtype not in dtypes:
         raise TypeError(f"{name} must have dtype in {dtypes}, got {t.dtype}")

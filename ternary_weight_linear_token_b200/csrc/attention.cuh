@@ -1,9 +1,10 @@
 // attention.cuh -- what the attention kernels over the 8-bit cache share.
 //
 // Here and in the other kernels of the decode step, what an earlier kernel may
-// have written is read through L2 (__ldcg) or by bulk copies: these kernels
-// start before that one has ended (programmatic dependent launch), so nothing
-// of it may come from a cache that was filled meanwhile.
+// have written is read after griddepcontrol.wait (these kernels start before
+// that one has ended), by plain loads, loads through L2 (__ldcg) or bulk
+// copies, never through the read-only path.  The exception is weights that the
+// caller calls static.
 #pragma once
 
 #include <cuda_fp16.h>
@@ -13,8 +14,6 @@
 
 namespace bitnet {
 
-constexpr int kStatusRange = 6;  // == BITNET_ERR_RANGE
-constexpr float kLog2e = 1.4426950408889634f;
 // Weights are 2^(score - m + kRaise); m follows the scores once they pass it
 // by kLazy (both log2): weights stay below 2^15, and fp16 keeps them to 2^-12
 // or to 2^-32 of the largest.
@@ -39,11 +38,6 @@ __device__ __forceinline__ int first_seen(int pos, int window) {
   return window > 0 && pos >= window ? pos - window + 1 : 0;
 }
 
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
 
 // 2^x down to fp32's smallest number (2^-149).
 __device__ __forceinline__ float ex2_whole(float x) {

@@ -14,10 +14,24 @@
 namespace bitnet {
 
 constexpr int kStatusTimeout = 5;  // == BITNET_ERR_TIMEOUT
+constexpr int kStatusRange = 6;    // == BITNET_ERR_RANGE
 
 // ------------------------------------------------------------ status word
 __device__ __forceinline__ void record_status(int *status, int code) {
   if (status != nullptr) atomicCAS(status, 0, code);
+}
+
+// ------------------------------------------------------------ arithmetic
+constexpr float kLog2e = 1.4426950408889634f;
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
 }
 
 // ------------------------------------------------------------ PDL

@@ -203,7 +203,6 @@ cudaError_t launch_w4(const void *X, int x_kind, const uint8_t *packed, const ui
                       bool weights_static, const LaunchCtx &ctx);
 
 // token_logprobs.cu
-constexpr int kLogprobsMaxTop = 32;
 cudaError_t launch_token_logprobs(const void *X, int x_kind, int64_t M, int64_t V, int64_t stride,
                                   const int64_t *tokens, int top, float *logprob, float *entropy,
                                   int64_t *top_ids, float *top_logprobs, const LaunchCtx &ctx);

@@ -23,7 +23,6 @@
 namespace bitnet {
 namespace {
 
-constexpr int kStatusRange = 6;  // == BITNET_ERR_RANGE
 constexpr int kMaxThreads = 256;
 constexpr int kMaxChunks = 8;    // 8-element chunks per thread: 128 x 128 values / 256 threads
 

@@ -137,11 +137,6 @@ __device__ __forceinline__ void tmem_arrived(uint32_t (&r)[32]) {
 }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-__device__ __forceinline__ float max3(float a, float b, float c) {
-  float r;
-  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
-  return r;
-}
 // Byte offset of 16-byte chunk `chunk` of row `row` of an operand tile of
 // `rows` rows, stored as panels of 64 halves (128-byte rows, 128-byte swizzle).
 __device__ __forceinline__ int operand_offset(int rows, int row, int chunk) {

@@ -29,10 +29,8 @@
 namespace bitnet {
 namespace {
 
-constexpr int kStatusRange = 6;  // == BITNET_ERR_RANGE
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
-constexpr float kLog2e = 1.4426950408889634f;
 
 struct LogprobParams {
   const void *x;
@@ -48,22 +46,12 @@ struct LogprobParams {
 struct Sums {
   float m, s, u;
 };
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
 // x - m, at least -1e28 (e^d is 0 there, and so is d e^d, times any sum); NaN
 // stays NaN.
 __device__ __forceinline__ float below(float x, float m) {
   float y;
   asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(__fsub_rn(x, m)), "f"(-1e28f));
   return y;
-}
-__device__ __forceinline__ float max3(float a, float b, float c) {
-  float r;
-  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
-  return r;
 }
 __device__ __forceinline__ float min3(float a, float b, float c) {
   float r;
