@@ -446,8 +446,9 @@ bitnet_status bitnet_decode_chain(const bitnet_chain_step *steps, int n_steps, c
  *            tokens' arrays are sequence b's last ones, in order, the last
  *            row at position lens[b] - 1.  NULL: one row per sequence (T ==
  *            B).  Rows behind offsets[B] belong to no sequence.
- *   max_new  the most new rows of a sequence, as the launch is sized by it;
- *            results do not depend on it.
+ *   max_new  the most new rows of a sequence: the launch is sized, and for
+ *            attention the kernel chosen, by it.  Any number gives results
+ *            within the same bounds.
  * What the kernels read there cannot be checked on the host: a sequence whose
  * offsets do not lie in 0..T, whose length is negative or above max_pages *
  * page_tokens, or (bitnet_kv_append) below its new rows is left alone, and a
@@ -568,8 +569,10 @@ bitnet_status bitnet_get_device_status(bitnet_stream_t stream);
 
 /* ABI version of this header: major * 10000 + minor * 100 + patch.  1.1:
  * the path query, the host-to-host call and its plans; the chain workspace
- * holds tagged link values (its size from bitnet_decode_chain_workspace_size). */
-#define BITNET_VERSION 10100
+ * holds tagged link values (its size from bitnet_decode_chain_workspace_size).
+ * 1.2: the 8-bit cache and attention over it, products with 4-bit weights,
+ * token log probabilities. */
+#define BITNET_VERSION 10200
 int bitnet_version(void);
 
 #ifdef __cplusplus

@@ -589,7 +589,9 @@ def bitnet_kv_append(cache: KVCache, K: torch.Tensor, V: torch.Tensor, pages: to
     pages [B, max_pages], lens [B] (the new tokens included) and offsets
     [B + 1] int32 say where: rows offsets[b] .. offsets[b + 1] - 1 are the
     last tokens of sequence b; without offsets each sequence has one row.
-    ``max_new``: the most rows of a sequence (default: T)."""
+    ``max_new``: the most rows of a sequence (default: T; the launch is sized
+    and, for attention, the kernel chosen by it: give it for several sequences
+    of few rows)."""
     kind = _FLOAT.get(K.dtype)
     if kind is None or V.dtype != K.dtype:
         raise TypeError(f"K and V must both be fp32 or bf16, got {K.dtype} and {V.dtype}")

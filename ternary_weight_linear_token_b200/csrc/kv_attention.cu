@@ -35,11 +35,13 @@
 // workspace: 10.5 against 14.8 us a call for one sequence of 700 tokens, 15.6
 // against 20.9 for 8 of 4000, 15.6 against 23.5 for 5 drafts each of 16 within
 // a window of 1024).
-// Bound by instruction issue: converting the codes takes some 380 of the 700
-// instructions that a chunk costs with its share of a CTA's start and end.  48
-// sequences of up to 4096 tokens (124 MB): 38 us, 3.3 TB/s; three CTAs per SM
-// with two stages against two with three: 44 against 48 us; pieces for 5 CTAs
-// per SM against 8: 40 against 44 us.
+// 48 sequences of up to 4096 tokens (124 MB): 39 us, 3.2 TB/s.  No unit is
+// full (counters: HBM 41 %, issue slots 43 %, ALU 37 %): 10 warps an SM (12 is
+// what registers and rings allow) wait in turn for their own results, shared
+// memory and copies, in 1.6 waves.  Converting the codes is some 380 of the 840
+// instructions that a chunk costs with its share of a CTA's start and end.
+// Three CTAs per SM with two stages against two with three: 44 against 48 us;
+// pieces for 5 CTAs per SM against 8: 40 against 44 us.
 #include <atomic>
 
 #include "attention.cuh"
@@ -747,6 +749,14 @@ struct AttnPlan {
   bool cluster;
 };
 constexpr int64_t kSms = 148;
+// A cluster of 8 spares the second launch but has longer pieces.  bf16, 20/5
+// heads of 128, cluster against pieces, us:
+//   span       256         1024         4096         8192         16384
+//   1 seq.   6.5 / 7.7   6.8 /  8.0  11.3 / 10.4  17.1 / 13.8  28.7 / 23.7
+//   4 seq.   6.7 / 7.7   8.2 /  9.6  13.8 / 18.9  21.2 / 25.6  35.3 / 35.3
+//   16 seq.  7.6 / 9.2  13.1 / 18.6  27.6 / 34.3  47.1 / 51.2  80.9 / 81.9
+// So up to a span of 4096 (and a window's or a page's rounding), where the
+// pieces are 512 tokens; with fewer CTAs a cluster, pieces of up to 1024.
 constexpr int64_t kClusterSpan = 4096 + 128, kClusterPiece = 1024 + 32;
 AttnPlan plan_of(const KvCache &cache, const KvBatch &batch, const AttnArgs &args) {
   AttnPlan a;
@@ -802,7 +812,15 @@ cudaError_t launch(const AttnParams &p, const AttnPlan &a, const LaunchCtx &ctx)
                   dim3(kWarps * 32), 0, ctx, p, a.rows);
 }
 
-// Prompts of bf16 queries go to the tcgen05 kernel.
+// Prompts of bf16 queries go to the tcgen05 kernel, by their rows alone.  One
+// sequence, 20/5 heads of 128, that kernel against the one above, us:
+//   new 32 of 2048      54 / 18      of 8192   178 /  43    of 60000  1261 /  148
+//   new 128 of 128      19 / 11      of 2048    63 /  35    of 60000  1417 /  535
+//   new 512 of 512      28 / 32      of 4096   110 / 197    of 60000  1417 / 2279
+//   new 2048 of 2048    67 / 185     new 4096 of 4096   159 / 591
+// It does not split the keys, so short prompts behind long prefixes, which leave
+// most SMs without a CTA, are better served by the other one; the rule does not
+// look at that.
 bool use_prompt(const KvCache &cache, const AttnArgs &args) {
   return args.kind == kBF16 && args.max_new * (args.q_heads / cache.heads) >= 128;
 }

@@ -22,11 +22,12 @@
 //                 tile's products
 // Tensor memory: S0 S1 (128 columns each, P over their first 64), O0 O1.
 // At head_dim 128 a block of 128 tokens has 2,048 clocks of exponentials (16 a
-// clock and SM) and 2,040 of tensor-core work.  Measured: about 6,500, of
-// which a tile's softmax takes 4,500 (its four warps are two per scheduler and
-// wait on their own latencies; knocking out the exponentials saves a tenth)
-// and the products behind it most of the rest: 224 us for prompts of 4096
-// tokens and 118 GFLOP (527 TFLOP/s).  Two threads per row and smaller
+// clock and SM) and 2,040 of tensor-core work.  Measured (clock64 in a copy):
+// about 6,500, of which a tile's softmax takes 4,500 (its four warps are two
+// per scheduler and wait on their own latencies; knocking out the exponentials
+// saves a tenth) and the products behind it most of the rest: 224 us for
+// prompts of 4096 and 1236 tokens and 118 GFLOP (527 TFLOP/s; counters: tensor
+// pipe 28 %, exponentials 28 %, issue slots 41 %).  Two threads per row and smaller
 // register sets (296 us) and weights before the maximum is known, redone
 // where it grows (243 us at the time of 245), were measured and not kept.
 // Every wait is bounded (common.cuh).

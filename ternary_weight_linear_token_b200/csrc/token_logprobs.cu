@@ -18,10 +18,12 @@
 // (from L2), a lane per chunk.  Warps keep the best 32 keys sorted, one per
 // lane, and join two such lists by a bitonic merge; CTAs of a cluster join
 // theirs through distributed shared memory.
-// A row of 128256 takes a CTA about 15 us, of which the selection's sorts and
-// barriers are a third: 701 bf16 rows 61 us (2.9 TB/s; three CTAs per SM with
-// batches of 2 chunks against two with batches of 4: 61 against 69 us), one
-// fp32 row over 8 CTAs 12 us, latency.
+// 701 bf16 rows of 128256: 62 us with the top 5 (2.9 TB/s, 1.6 waves), 45 us
+// without a selection, whose sorts and barriers have no loads in flight
+// (counters: issue slots 58 %, ALU 42 %, exponentials 37 %, HBM 36 %); three
+// CTAs per SM with batches of 2 chunks against two with batches of 4: 61
+// against 69 us.  One fp32 row over 8 CTAs: 12.9 us with the top 20, 6.0
+// without, latency.
 #include "common.cuh"
 #include "internal.h"
 #include "pairs.cuh"
