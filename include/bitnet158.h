@@ -570,9 +570,10 @@ bitnet_status bitnet_get_device_status(bitnet_stream_t stream);
 /* ABI version of this header: major * 10000 + minor * 100 + patch.  1.1:
  * the path query, the host-to-host call and its plans; the chain workspace
  * holds tagged link values (its size from bitnet_decode_chain_workspace_size).
- * 1.2: the 8-bit cache and attention over it, products with 4-bit weights,
- * token log probabilities. */
-#define BITNET_VERSION 10200
+ * The 8-bit cache and attention over it, products with 4-bit weights and token
+ * log probabilities came under the same number: functions were added, none
+ * changed. */
+#define BITNET_VERSION 10100
 int bitnet_version(void);
 
 #ifdef __cplusplus
