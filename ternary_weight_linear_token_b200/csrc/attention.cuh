@@ -15,8 +15,8 @@
 namespace bitnet {
 
 // Weights are 2^(score - m + kRaise); m follows the scores once they pass it
-// by kLazy (both log2): weights stay below 2^15, and fp16 keeps them to 2^-12
-// or to 2^-32 of the largest.
+// by kLazy (both log2): weights stay below 2^15, and fp16 keeps them to 2^-11
+// or to 2^-32 of the largest (2^-31 for prompts, whose m is whole).
 constexpr float kLazy = 8.0f;
 constexpr float kRaise = 7.0f;
 

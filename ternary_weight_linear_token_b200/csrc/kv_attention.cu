@@ -22,7 +22,7 @@
 // running maximum m of that sum, so O += p' vc needs no further scale, while
 // the row sum adds p' / vs.  A page of zeros (vs = 0) counts with log2 vs =
 // -60 (scales far apart: attention.cuh).  p' is held 2^kRaise higher, and m may
-// lag behind by kLazy: p' stays below 2^15, and fp16 rounds it by at most 2^-12
+// lag behind by kLazy: p' stays below 2^15, and fp16 rounds it by at most 2^-11
 // of itself or, below fp16's normal numbers, by 2^-25: 2^-32 of the largest
 // weight.
 //
